@@ -43,8 +43,8 @@ enum {
 };
 
 /* Sizes.  Supported: dh in {16, 32, 64, 128}; block in {16, 32, 64, 128};
- * 1 <= Hkv, Hq a multiple of Hkv, Hq <= 1024; n_blocks * Hkv < 2^31;
- * max_blocks * block < 2^31.  The cache itself may pass 2^32 bytes. */
+ * 1 <= Hkv, Hq a multiple of Hkv, Hq <= 1024; 1 <= n_blocks, n_blocks * Hkv <
+ * 2^31; max_blocks * block <= 2^30.  The cache may pass 2^32 bytes. */
 typedef struct {
   int32_t Hq;         /* query heads                                           */
   int32_t Hkv;        /* key/value heads; query head h reads head h*Hkv/Hq     */
@@ -131,12 +131,14 @@ int lime_kv_append(const lime_kv_dims* dims, const void* K, int64_t ldk, const v
  *                the rows j <= lens[u] - m + i
  *   O            device [total_q, Hq, dh], contiguous
  *   lse          device fp32 [total_q, Hq] or NULL: log of the softmax's sum
- * A query that sees no row gets a zero output and lse = -inf.  Scores, sums
- * and outputs are fp32; the probabilities enter the value product as fp16
- * scaled by 2^15, relative to the row's largest (fp32 dtype: as two fp16
- * terms), so weights below 2^-39 of the largest are lost.  Codes behind a
- * request's last row are never used.  A table entry outside the pool hides its
- * rows and sets LIME_FLAG_BAD_BLOCK. */
+ * |sm_scale| <= 2^100; scales are finite and not negative.  A query that sees
+ * no row gets a zero output and lse = -inf.  Scores, sums and outputs are fp32.
+ * Queries enter the score product exactly (bf16) or as two fp16 terms (fp32);
+ * probabilities enter the value product as one fp16 term (bf16 dtype) or two
+ * (fp32), relative to the row's largest, to 2^-39 of which they are exact: what
+ * a row's tail below that weighs is lost.  Codes behind a request's last row
+ * are never used.  A table entry outside the pool hides its rows and sets
+ * LIME_FLAG_BAD_BLOCK. */
 int lime_kv_attention(const lime_kv_dims* dims, int64_t B, const void* Q, int64_t ldq,
                       const int64_t* q_offsets, int64_t total_q, const int32_t* block_table,
                       const int32_t* lens, const int8_t* k_cache, const int8_t* v_cache,

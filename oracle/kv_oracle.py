@@ -79,12 +79,12 @@ def append(x, slots, codes, scale, bs):
 def attention(q, q_counts, table, lens, k, v, scale, bs, sm_scale, causal):
     """q fp64 [n, Hq, dh]; codes and fp64 scale [blocks, Hkv, 2].
 
-    Returns (O, lse, A, S): A = sum_j w_j |v_j| and S = max_j sum_d |q_d k_jd|
-    sm_scale, the magnitudes an error bound of O and lse needs."""
+    Returns (O, lse, A, S, V): A = sum_j w_j |v_j|, V = max_j |v_j| and S = max_j
+    sum_d |q_d k_jd| sm_scale, the magnitudes an error bound of O and lse needs."""
     n_rows, Hq, dh = q.shape
     G = Hq // k.shape[1]
     O, lse = np.zeros((n_rows, Hq, dh)), np.full((n_rows, Hq), -np.inf)
-    A, S = np.zeros((n_rows, Hq, dh)), np.zeros((n_rows, Hq))
+    A, S, V = np.zeros((n_rows, Hq, dh)), np.zeros((n_rows, Hq)), np.zeros((n_rows, Hq, dh))
     i = 0
     for u, m in enumerate(map(int, q_counts)):
         n = int(lens[u])
@@ -101,7 +101,7 @@ def attention(q, q_counts, table, lens, k, v, scale, bs, sm_scale, causal):
                     w = np.exp(s - top)
                     lse[i, h] = top + np.log(w.sum())
                     w /= w.sum()
-                    O[i, h], A[i, h] = w @ vv, w @ np.abs(vv)
+                    O[i, h], A[i, h], V[i, h] = w @ vv, w @ np.abs(vv), np.abs(vv).max(0)
                     S[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * abs(sm_scale)
             i += 1
-    return O, lse, A, S
+    return O, lse, A, S, V

@@ -14,11 +14,11 @@ constexpr size_t kStatusBytes = 256;  // status word + padding at the workspace 
 
 int check_dims(const lime_kv_dims* D) {
   if (!D || (D->dtype != LIME_F32 && D->dtype != LIME_BF16)) return LIME_ERR_ARG;
-  if (D->Hq <= 0 || D->Hkv <= 0 || D->max_blocks <= 0 || D->n_blocks < 0) return LIME_ERR_ARG;
+  if (D->Hq <= 0 || D->Hkv <= 0 || D->max_blocks <= 0 || D->n_blocks <= 0) return LIME_ERR_ARG;
   if (D->Hq % D->Hkv != 0 || D->Hq > 1024) return LIME_ERR_SHAPE;
   if (D->dh != 16 && D->dh != 32 && D->dh != 64 && D->dh != 128) return LIME_ERR_SHAPE;
   if (D->block != 16 && D->block != 32 && D->block != 64 && D->block != 128) return LIME_ERR_SHAPE;
-  if (D->n_blocks > INT32_MAX / D->Hkv || D->max_blocks > INT32_MAX / D->block)
+  if (D->n_blocks > INT32_MAX / D->Hkv || D->max_blocks > (1 << 30) / D->block)
     return LIME_ERR_SHAPE;
   return LIME_OK;
 }
@@ -185,15 +185,15 @@ int lime_kv_attention(const lime_kv_dims* dims, int64_t B, const void* Q, int64_
                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   int rc = check_dims(dims);
   if (rc) return rc;
-  if (bad_count(B) || bad_count(total_q) || (causal != 0 && causal != 1) || !isfinite(sm_scale))
+  if (bad_count(B) || bad_count(total_q) || (causal != 0 && causal != 1) || !(fabsf(sm_scale) <= 0x1p100f))
     return LIME_ERR_ARG;
   // rows of all heads are counted in 32 bits
   if (total_q * dims->Hq > INT32_MAX) return LIME_ERR_ARG;
   if ((rc = check_ws(workspace, workspace_bytes, dims, B, total_q))) return rc;
   if (B == 0) return total_q == 0 ? LIME_OK : LIME_ERR_ARG;
   if (total_q == 0) return LIME_OK;
-  if (!Q || !q_offsets || !block_table || !lens || !O) return LIME_ERR_ARG;
-  if (dims->n_blocks > 0 && (!k_cache || !v_cache || !scale)) return LIME_ERR_ARG;
+  if (!Q || !q_offsets || !block_table || !lens || !k_cache || !v_cache || !scale || !O)
+    return LIME_ERR_ARG;
   const size_t es = esize(dims);
   const int64_t width = (int64_t)dims->Hq * dims->dh;
   if (ldq < width || ldq > INT32_MAX || ldq * es % 16 != 0) return LIME_ERR_ARG;

@@ -1,108 +1,818 @@
-// Attention over the paged 8-bit history cache.
+// Attention over the paged 8-bit history cache (include/lime_kv.h).
+//
+// A pair is one (request, kv head, tile of R query rows).  Its cached rows are
+// cut into tiles of TK keys; all pairs' tiles, laid end to end, are divided
+// evenly over the thread blocks (k_kv_plan), so that ragged requests load
+// every SM alike.  A block's share of one pair is a segment; the block's warps
+// take the segment's tiles in turn, each with its own softmax state and its own
+// ring of TMA stages, and join their states at the segment's end.  A pair cut
+// by block borders leaves partial results, which the last block to finish joins
+// in the blocks' order.
+//
+// Both products run on mma.sync with fp16 operands and fp32 sums.  A code is
+// exact in fp16, and becomes a matrix fragment in registers: the byte under the
+// exponent of 1024 (0x64) is 1024 + code + 128, less 1152.  tcgen05 reads its
+// operands from shared memory or TMEM, which would add a store and a load of
+// two bytes for every code read once; here a code goes from the ring straight
+// into the fragment.  Which key a fragment's column stands for, and which dims
+// a lane holds, are free as long as both products agree; KeyMap picks them so
+// that every shared-memory read is a wide one without bank conflicts.
 #include <math.h>
 
+#include "lime_fast.cuh"
 #include "lime_kv.cuh"
+#include "sm100.cuh"
 
 namespace lime {
 
+using namespace sm100;
+
 namespace {
 
-// One warp per (query row, head): 32 keys at a time, a key per lane for the
-// scores and a few dims per lane for the values, with the running maximum and
-// sum of the softmax.
-template <class T, int DH>
-__global__ void k_attn_rows(lime_kv_dims D, int64_t B, const T* Q, int64_t ldq, const int64_t* off,
-                            int64_t total_q, const int32_t* table, const int32_t* lens,
-                            const int8_t* kc, const int8_t* vc, const float* scale, float sm_scale,
-                            bool causal, T* O, float* lse, unsigned* status) {
-  constexpr int PER = (DH + 31) / 32;
-  __shared__ float qs[4][DH];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * 4 + warp;
-  if (r >= total_q * D.Hq) return;
-  const int64_t i = r / D.Hq;
-  const int hq = (int)(r % D.Hq), h = hq / (D.Hq / D.Hkv);
-  const int64_t u = owner_of(off, B, i);
-  int64_t a, b;
-  user_range(off, u, B, total_q, &a, &b, status);
-  const int n = kv_len(lens, u, (int64_t)D.max_blocks * D.block, status);
-  int64_t limit = causal ? n - (b - a) + (i - a) + 1 : n;
-  if (limit > n) limit = n;
-  for (int d = lane; d < DH; d += 32) qs[warp][d] = to_f(Q[i * ldq + (int64_t)hq * DH + d]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.0f, o[PER];
-  for (int k = 0; k < PER; ++k) o[k] = 0.0f;
-  for (int64_t j0 = 0; j0 < limit; j0 += 32) {
-    const int64_t j = j0 + lane;
-    float s = -INFINITY, vs = 0.0f;
-    int64_t base = -1;
-    if (j < limit) {
-      const int64_t block = table[u * D.max_blocks + j / D.block];
-      if (block >= 0 && block < D.n_blocks) {
-        base = ((block * D.Hkv + h) * D.block + j % D.block) * DH;
-        const float2 sc = reinterpret_cast<const float2*>(scale)[block * D.Hkv + h];
-        float acc = 0.0f;
-        for (int d = 0; d < DH; ++d) acc += qs[warp][d] * (float)kc[base + d];
-        s = acc * sc.x * sm_scale;
-        vs = sc.y;
-      } else {
-        raise_flag(status, LIME_FLAG_BAD_BLOCK);
-      }
-    }
-    const float top = fmaxf(m, warp_max(s));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    const float p = expf(s - ref), keep = expf(m - ref);
-    m = top;
-    l = l * keep + warp_sum(p);
-    const float pv = p * vs;
-    for (int k = 0; k < PER; ++k) o[k] *= keep;
-    for (int t = 0; t < 32; ++t) {
-      const float w = __shfl_sync(0xffffffffu, pv, t);
-      const int64_t at = __shfl_sync(0xffffffffu, base, t);
-      if (at < 0) continue;
-      for (int k = 0; k < PER; ++k)
-        if (lane + 32 * k < DH) o[k] += w * (float)vc[at + lane + 32 * k];
-    }
-  }
-  for (int k = 0; k < PER; ++k)
-    if (lane + 32 * k < DH) O[r * DH + lane + 32 * k] = from_f<T>(l > 0.0f || l != l ? o[k] / l : 0.0f);
-  if (lse && lane == 0) lse[r] = m + logf(l);
+constexpr int kWarps = 4;
+constexpr int kMaxCtas = 640;       // most blocks of the persistent grid
+constexpr int kPairCost = 4;        // a pair's fixed cost, in tiles
+constexpr float kOffset = 14.0f;    // probabilities enter fp16 times 2^14
+constexpr float kTiny = 1e-37f;     // least factor of a score: -inf times 0 would be NaN
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Per head dim: keys of a warp's tile and stages of its ring.
+template <int DH> struct Tile {
+  static constexpr int TK = DH == 128 ? 32 : 64;
+  static constexpr int kStages = DH == 128 ? 3 : DH == 64 ? 3 : 4;
+  static constexpr int kBytes = TK * DH;             // keys (or values) of a tile
+  static constexpr int kRing = kStages * 2 * kBytes; // per warp
+};
+
+struct Plan {
+  int64_t total;  // weight of all pairs: tiles plus kPairCost each
+  int64_t share;  // weight of one block
+};
+
+struct Args {
+  const void* Q;
+  int64_t ldq;
+  const int64_t* off;
+  const int32_t* table;
+  const int32_t* lens;
+  const float2* scale;
+  const Plan* plan;
+  const int64_t* prefix;  // [B + 1] weight before each request
+  int* tickets;           // [grid]
+  float* part;            // [2 * grid] partial results
+  void* O;
+  float* lse;
+  unsigned* status;
+  int64_t B, total_q, n_blocks;
+  int Hq, Hkv, G, block, max_blocks;
+  float scale_log2;  // |sm_scale| log2 e
+  bool negative;     // sm_scale < 0
+  bool causal;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <class T>
-void launch(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, const int64_t* off,
-            int64_t total_q, const int32_t* table, const int32_t* lens, const int8_t* kc,
-            const int8_t* vc, const float* scale, float sm_scale, bool causal, void* O, float* lse,
-            unsigned* status, cudaStream_t st) {
-  const unsigned grid = (unsigned)ceil_div(total_q * D.Hq, 4);
-#define LAUNCH(DH)                                                                             \
-  k_attn_rows<T, DH><<<grid, 128, 0, st>>>(D, B, (const T*)Q, ldq, off, total_q, table, lens, \
-                                           kc, vc, scale, sm_scale, causal, (T*)O, lse, status)
-  if (D.dh == 16) LAUNCH(16);
-  else if (D.dh == 32) LAUNCH(32);
-  else if (D.dh == 64) LAUNCH(64);
-  else LAUNCH(128);
-#undef LAUNCH
-  note_launches(1);
+// ------------------------------------------------------------------- plan
+
+// Prefix sums of the requests' weights, the blocks' share and cleared tickets.
+__global__ void __launch_bounds__(1024)
+    k_kv_plan(int64_t B, const int64_t* off, int64_t total_q, const int32_t* lens, int Hkv, int G,
+              int64_t most, int R, int TK, int grid, Plan* plan, int64_t* prefix, int* tickets,
+              unsigned* status) {
+  __shared__ int64_t part[32];
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < grid; i += blockDim.x) tickets[i] = 0;
+  const int64_t per = ceil_div(B, 1024);
+  const int64_t u0 = per * threadIdx.x, u1 = u0 + per < B ? u0 + per : B;
+  int64_t sum = 0;
+  for (int64_t u = u0; u < u1; ++u) {
+    int64_t a, b;
+    user_range(off, u, B, total_q, &a, &b, status);
+    const int n = kv_len(lens, u, most, status);
+    const int64_t w = ceil_div((b - a) * G, R) * Hkv * (ceil_div(n, TK) + kPairCost);
+    prefix[u] = w;
+    sum += w;
+  }
+  int64_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t p = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, p, o);
+      if (lane >= o) p += y;
+    }
+    part[lane] = p;
+  }
+  __syncthreads();
+  int64_t at = (warp ? part[warp - 1] : 0) + x - sum;
+  for (int64_t u = u0; u < u1; ++u) {
+    const int64_t w = prefix[u];
+    prefix[u] = at;
+    at += w;
+  }
+  if (threadIdx.x == 0) {
+    const int64_t all = part[31];
+    prefix[B] = all;
+    plan->total = all;
+    // a share below one tile per warp would only add joins
+    const int64_t share = ceil_div(all, grid), least = kPairCost + kWarps;
+    plan->share = share > least ? share : least;
+  }
+}
+
+// The request whose weights hold position s: the largest u with prefix[u] <= s
+// (a warp probes 32 places at a time).
+__device__ __forceinline__ int64_t find_request(const int64_t* prefix, int64_t B, int64_t s) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = B;  // answer in [lo, hi)
+  while (hi - lo > 1) {
+    const int64_t step = ceil_div(hi - lo, 32);
+    const int64_t p = lo + step * lane;
+    const bool ok = p < hi && prefix[p] <= s;
+    const int n = __popc(__ballot_sync(0xffffffffu, ok));  // n >= 1
+    lo += step * (n - 1);
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  return lo;
+}
+
+// -------------------------------------------------------------- fragments
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The same, the largest finite fp16 in place of an overflow (a probability's
+// exponent is off by more than 2 once scores pass 2^25).
+__device__ __forceinline__ uint32_t half2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// {1024 + b0, 1024 + b1} - 1152 of two biased bytes (code + 128) picked by SEL.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
+  const uint32_t m = __byte_perm(w, 0x64646464u, SEL);
+  const uint32_t bias = 0x64806480u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&m),
+                            *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Byte offset inside a tile, through the 128-byte swizzle the TMA applies.
+__device__ __forceinline__ uint32_t swz(uint32_t off) { return off ^ (((off >> 7) & 7u) << 4); }
+
+// Which of 16 keys a fragment's columns stand for.  Column c of the first
+// (second) 8-key product is key col(c) (col(c) + odd): lane t of a quad then
+// holds in both products the scores, and as value rows the codes, of keys
+// key(t, 0..3).  With the tiles' swizzle, no two lanes of a shared-memory
+// access phase meet in a bank, for the key reads (a row per lane group g) and
+// for the value reads (a row per lane t).
+template <int DH> struct KeyMap {
+  static constexpr int odd = DH == 64 ? 2 : 8;
+  __device__ static __forceinline__ int col(int c) {
+    const int t = c >> 1;
+    if (DH == 64) return 4 * t + (c & 1);
+    if (DH == 32) return (c & 1) ? 4 + (t ^ 2) : t;
+    return c;
+  }
+  __device__ static __forceinline__ int key(int t, int i) { return col(2 * t + (i & 1)) + (i >> 1) * odd; }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
+  if constexpr (BYTES == 16) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+  } else if constexpr (BYTES == 8) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  } else if constexpr (BYTES == 4) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+  } else {
+    asm volatile("{.reg .b16 x; ld.shared.b16 x, [%1]; cvt.u32.u16 %0, x;}"
+                 : "=r"(w[0])
+                 : "r"(addr)
+                 : "memory");
+  }
+}
+
+// ----------------------------------------------------------------- kernel
+
+template <typename T, int DH, int MT>
+__global__ void __launch_bounds__(kWarps * 32)
+    k_kv_attn(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+              const Args a) {
+  constexpr bool kSplit = sizeof(T) == 4;  // fp32 rows: operands as two fp16 terms
+  constexpr int NQ = kSplit ? 2 : 1;
+  constexpr int TK = Tile<DH>::TK, S = Tile<DH>::kStages, NG = TK / 16;
+  constexpr int R = 16 * MT;
+  constexpr int KS = DH / 16;              // k-steps of the score product
+  constexpr int NT = DH / 8;               // 8-dim tiles of the output
+  constexpr int E = DH / 4;                // dims of a lane
+  constexpr int VB = DH / 8;               // value bytes of a lane and key
+  typedef KeyMap<DH> Map;
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kWarps][S];
+  __shared__ float2 ml[kWarps][R];
+  __shared__ int abort_flag, is_last;
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * Tile<DH>::kRing;
+  const uint32_t ring_u32 = smem_u32(ring);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+  }
+  if (lane == 0)
+    for (int s = 0; s < S; ++s) mbar_init(&full[warp][s], 1);
+  fence_mbar_init();
+  __syncthreads();
+  pdl_launch();
+  pdl_wait();
+
+  const int64_t share = a.plan->share, total = a.plan->total;
+  int64_t pos = share * blockIdx.x;
+  const int64_t pos_end = pos + share < total ? pos + share : total;
+  if (pos >= pos_end) return;
+  int64_t u = find_request(a.prefix, a.B, pos);
+
+  const int bs = a.block;
+  const int nb = bs >= TK ? 1 : TK / bs;   // blocks of a tile
+  const int box_rows = bs >= TK ? TK : bs;
+  const uint32_t box_bytes = (uint32_t)box_rows * DH;
+  const int batch = 32 / nb;               // tiles whose table entries a warp holds
+
+  // byte offsets of this lane's reads inside a 16-key group (the swizzle
+  // depends on the group only through whole 1024-byte rows and a constant)
+  const int kcol = Map::col(g);
+  uint32_t stage = 0, phase = 0;           // of the ring; phase: one bit per stage
+
+  while (pos < pos_end) {
+    while (a.prefix[u + 1] <= pos) ++u;
+    int64_t q0, q1;
+    user_range(a.off, u, a.B, a.total_q, &q0, &q1, a.status);
+    const int m_rows = (int)(q1 - q0);
+    const int n = kv_len(a.lens, u, (int64_t)a.max_blocks * bs, a.status);
+    const int tiles = (n + TK - 1) / TK;
+    const int rts = (int)ceil_div((int64_t)m_rows * a.G, R);
+    const int64_t w_pair = tiles + kPairCost;
+    const int64_t local = pos - a.prefix[u];
+    const int64_t pair = local / w_pair;
+    const int64_t pair_pos = pos - (local - pair * w_pair);  // where the pair begins
+    const int64_t seg_end = pair_pos + w_pair < pos_end ? pair_pos + w_pair : pos_end;
+    const int h = (int)(pair / rts), rt = (int)(pair % rts);
+    int t0 = (int)(pos - pair_pos) - kPairCost, t1 = (int)(seg_end - pair_pos) - kPairCost;
+    if (t0 < 0) t0 = 0;
+    if (t1 < 0) t1 = 0;
+
+    // the rows' limits: row r sees keys below limit(r)
+    const int r_base = rt * R, rows = m_rows * a.G - r_base < R ? m_rows * a.G - r_base : R;
+    auto limit_of = [&](int r) {
+      if (!a.causal) return n;
+      const int lim = n - m_rows + (r_base + r) / a.G + 1;
+      return lim < 0 ? 0 : lim;
+    };
+    const int lim_low = limit_of(0), lim_high = limit_of(rows - 1);
+    const int t_live = (lim_high + TK - 1) / TK;
+    if (t1 > t_live) t1 = t_live;
+
+    // ---- queries: fp16 fragments of rows scaled to [2^14, 2^15)
+    uint32_t qf[MT][KS][NQ][4];
+    float c_row[MT][2];
+    int lim[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = mt * 16 + hf * 8 + g;
+        float x[E];
+        if (r < rows) {
+          const int rr = r_base + r;
+          const T* src = (const T*)a.Q + (q0 + rr / a.G) * a.ldq +
+                         (int64_t)(h * a.G + rr % a.G) * DH + E * t;
+#pragma unroll
+          for (int d = 0; d < E; d += 16 / (int)sizeof(T) > E ? E : 16 / (int)sizeof(T)) {
+            if constexpr (sizeof(T) == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(src + d);
+              x[d] = v.x, x[d + 1] = v.y, x[d + 2] = v.z, x[d + 3] = v.w;
+            } else if constexpr (E >= 8) {
+              unpack8(*reinterpret_cast<const uint4*>(src + d), x + d);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(src + d);
+              const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+              const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+              x[d] = f0.x, x[d + 1] = f0.y, x[d + 2] = f1.x, x[d + 3] = f1.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < E; ++d) x[d] = 0.0f;
+        }
+        lim[mt][hf] = r < rows ? limit_of(r) : 0;
+        float top = 0.0f;
+#pragma unroll
+        for (int d = 0; d < E; ++d) top = fmaxf(top, fabsf(x[d]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e <= top < 2^(e+1); times 2^(14-e) in two exact factors
+        const int e = top > 0.0f ? ilogbf(fminf(top, 3.402823466e38f)) : 14;
+        const int e1 = (14 - e) / 2, e2 = 14 - e - e1;
+        const float s1 = __int_as_float((e1 + 127) << 23) * (a.negative ? -1.0f : 1.0f);
+        const float s2 = __int_as_float((e2 + 127) << 23);
+        c_row[mt][hf] = a.scale_log2 / __int_as_float((e1 + 127) << 23) / s2;
+#pragma unroll
+        for (int w = 0; w < KS; ++w) {
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = x[4 * w + i] * s1 * s2;
+          const uint32_t h0 = half2_of(y[0], y[1]), h1 = half2_of(y[2], y[3]);
+          qf[mt][w][0][hf] = h0;
+          qf[mt][w][0][hf + 2] = h1;
+          if constexpr (kSplit) {
+            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            qf[mt][w][NQ - 1][hf] = half2_of(y[0] - f0.x, y[1] - f0.y);
+            qf[mt][w][NQ - 1][hf + 2] = half2_of(y[2] - f1.x, y[3] - f1.y);
+          }
+        }
+      }
+    }
+
+    float o[MT][NT][4], m[MT][2], l[MT][2], vref = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.0f;
+    }
+
+    // ---- table entries and scales of 32 / nb tiles ahead, one block per lane
+    const int count = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
+    const int n_cols = (n + bs - 1) / bs;
+    auto load_batch = [&](int first, int& ent, float2& sc) {
+      const int j = first + lane / nb;
+      ent = -1;
+      sc = make_float2(-1.0f, 0.0f);     // a negative key scale hides the block
+      if (j < count && lane < batch * nb) {
+        const int64_t key = (int64_t)(t0 + warp + j * kWarps) * TK;
+        const int64_t col = key / bs + lane % nb;
+        if (col < n_cols) {
+          const int b = a.table[u * a.max_blocks + col];
+          if (b >= 0 && b < a.n_blocks) {
+            ent = b;
+            sc = a.scale[(int64_t)b * a.Hkv + h];
+          } else {
+            raise_flag(a.status, LIME_FLAG_BAD_BLOCK);
+          }
+        }
+      }
+    };
+    int ent0, ent1;
+    float2 sc0, sc1;
+    load_batch(0, ent0, sc0);
+    load_batch(batch, ent1, sc1);
+    int base = 0;                        // first tile of batch 0
+
+    // tile j goes to ring stage `st`
+    auto issue = [&](int j, uint32_t st) {
+      const int src = (j - base) * nb + lane % nb;
+      const int b0 = __shfl_sync(0xffffffffu, ent0, src & 31);
+      const int b1 = __shfl_sync(0xffffffffu, ent1, src & 31);
+      const int b = src < batch * nb ? b0 : b1;
+      const bool ok = lane < nb && b >= 0;
+      const unsigned live = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0)
+        mbar_arrive_expect_tx(&full[warp][st], (uint32_t)__popc(live) * box_bytes * 2);
+      __syncwarp();
+      if (ok) {
+        const int row = bs >= TK ? (int)(((int64_t)(t0 + warp + j * kWarps) * TK) % bs) * DH / 128 : 0;
+        uint8_t* dst = ring + st * 2 * Tile<DH>::kBytes + lane * box_bytes;
+        const int z = b * a.Hkv + h;
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+            "l"((uint64_t)&map_k), "r"(0), "r"(row), "r"(z), "r"(smem_u32(&full[warp][st]))
+            : "memory");
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst + Tile<DH>::kBytes)),
+            "l"((uint64_t)&map_v), "r"(0), "r"(row), "r"(z), "r"(smem_u32(&full[warp][st]))
+            : "memory");
+      }
+    };
+
+    {
+      uint32_t st = stage;
+      for (int j = 0; j < S && j < count; ++j) {
+        issue(j, st);
+        st = st + 1 == S ? 0 : st + 1;
+      }
+    }
+
+    for (int j = 0; j < count; ++j) {
+      if (j - base == batch) {           // batch 0 is used up
+        base += batch;
+        ent0 = ent1;
+        sc0 = sc1;
+        load_batch(base + batch, ent1, sc1);
+      }
+      const uint32_t ks = ring_u32 + stage * 2 * Tile<DH>::kBytes, vs = ks + Tile<DH>::kBytes;
+      mbar_wait(&full[warp][stage], (phase >> stage) & 1u, a.status, &abort_flag);
+      phase ^= 1u << stage;
+
+      // ---- scores
+      float s[MT][2 * NG][4];
+#pragma unroll
+      for (int x = 0; x < 2 * NG; ++x) {
+        const int key = (x >> 1) * 16 + kcol + (x & 1) * Map::odd;
+        uint32_t w[KS];
+        if constexpr (E >= 16) {
+#pragma unroll
+          for (int c = 0; c < E; c += 16) lds<16>(ks + swz(key * DH + E * t + c), w + c / 4);
+        } else {
+          lds<E>(ks + swz(key * DH + E * t), w);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][x][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t b = w[k] ^ 0x80808080u;
+          const uint32_t b0 = codes_to_half2<0x4140>(b), b1 = codes_to_half2<0x4342>(b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int p = 0; p < NQ; ++p) mma16816(s[mt][x], qf[mt][k][p], b0, b1);
+        }
+      }
+
+      // ---- the groups' scales; hidden keys
+      float kg[NG], vg[NG];
+      bool hidden = false;
+      float vmax = 0.0f;
+#pragma unroll
+      for (int x = 0; x < NG; ++x) {
+        const int src = (j - base) * nb + (nb > 1 ? x * 16 / bs : 0);
+        kg[x] = __shfl_sync(0xffffffffu, sc0.x, src);
+        vg[x] = __shfl_sync(0xffffffffu, sc0.y, src);
+        hidden |= kg[x] < 0.0f;
+        vmax = fmaxf(vmax, vg[x]);
+      }
+      const int key0 = (t0 + warp + j * kWarps) * TK;
+      if (hidden || key0 + TK > lim_low) {
+#pragma unroll
+        for (int x = 0; x < 2 * NG; ++x) {
+          const int key = key0 + (x >> 1) * 16 + (x & 1) * Map::odd;
+          const bool off = kg[x >> 1] < 0.0f;
+          const int ka = key + Map::col(2 * t), kb = key + Map::col(2 * t + 1);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            if (off || ka >= lim[mt][0]) s[mt][x][0] = -INFINITY;
+            if (off || kb >= lim[mt][0]) s[mt][x][1] = -INFINITY;
+            if (off || ka >= lim[mt][1]) s[mt][x][2] = -INFINITY;
+            if (off || kb >= lim[mt][1]) s[mt][x][3] = -INFINITY;
+          }
+        }
+        // the marker is no factor
+#pragma unroll
+        for (int x = 0; x < NG; ++x)
+          if (kg[x] < 0.0f) kg[x] = 1.0f;
+      }
+
+      // ---- running maximum (in units of log2) and value unit
+      float top[MT][2];
+      bool grow = vmax > vref;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float best = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < NG; ++x) {
+            const float v = fmaxf(fmaxf(s[mt][2 * x][2 * hf], s[mt][2 * x][2 * hf + 1]),
+                                  fmaxf(s[mt][2 * x + 1][2 * hf], s[mt][2 * x + 1][2 * hf + 1]));
+            best = fmaxf(best, v * fmaxf(c_row[mt][hf] * kg[x], kTiny));
+          }
+          top[mt][hf] = best;
+          grow |= best > m[mt][hf];
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        const float vnew = fmaxf(vref, vmax);
+        const float vkeep = vnew > 0.0f ? vref / vnew : 0.0f;
+        vref = vnew;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float v = top[mt][hf];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            v = fmaxf(v, m[mt][hf]);
+            const float keep = ex2(m[mt][hf] - (v == -INFINITY ? 0.0f : v));
+            m[mt][hf] = v;
+            l[mt][hf] *= keep;
+            const float ok = keep * vkeep;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              o[mt][i][2 * hf] *= ok;
+              o[mt][i][2 * hf + 1] *= ok;
+            }
+          }
+        }
+      }
+
+      // ---- probabilities times their block's value scale over the unit
+      uint32_t pf[MT][NG][NQ][4];
+#pragma unroll
+      for (int x = 0; x < NG; ++x) {
+        // log2 of the ratio, at least 2^-60 (what is smaller adds nothing)
+        const float lr = vref > 0.0f ? fmaxf(__log2f(vg[x] / vref), -60.0f) : 0.0f;
+        const float inv = ex2(-lr);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float c = fmaxf(c_row[mt][hf] * kg[x], kTiny);
+            const float add = kOffset + lr - (m[mt][hf] == -INFINITY ? 0.0f : m[mt][hf]);
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = s[mt][2 * x + (i >> 1)][2 * hf + (i & 1)];
+              p[i] = ex2(fmaf(v, c, add));
+            }
+            l[mt][hf] = fmaf((p[0] + p[1]) + (p[2] + p[3]), inv, l[mt][hf]);
+            const uint32_t h0 = half2_sat(p[0], p[1]), h1 = half2_sat(p[2], p[3]);
+            pf[mt][x][0][hf] = h0;
+            pf[mt][x][0][hf + 2] = h1;
+            if constexpr (kSplit) {
+              const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+              const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+              pf[mt][x][NQ - 1][hf] = half2_of(p[0] - f0.x, p[1] - f0.y);
+              pf[mt][x][NQ - 1][hf + 2] = half2_of(p[2] - f1.x, p[3] - f1.y);
+            }
+          }
+        }
+      }
+
+      // ---- values
+#pragma unroll
+      for (int x = 0; x < NG; ++x) {
+        constexpr int W = VB < 4 ? 1 : VB / 4;
+        uint32_t w[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lds<VB>(vs + swz((x * 16 + Map::key(t, i)) * DH + VB * g), w[i]);
+#pragma unroll
+          for (int c = 0; c < W; ++c) w[i][c] ^= 0x80808080u;
+        }
+#pragma unroll
+        for (int c = 0; c < W; ++c) {
+          // bytes of two keys side by side, two dims at a time
+          const uint32_t ab0 = __byte_perm(w[0][c], w[1][c], 0x5140), cd0 = __byte_perm(w[2][c], w[3][c], 0x5140);
+          const uint32_t ab1 = __byte_perm(w[0][c], w[1][c], 0x7362), cd1 = __byte_perm(w[2][c], w[3][c], 0x7362);
+#pragma unroll
+          for (int i = 0; i < (VB < 4 ? VB : 4); ++i) {
+            const uint32_t ab = i < 2 ? ab0 : ab1, cd = i < 2 ? cd0 : cd1;
+            const uint32_t b0 = (i & 1) ? codes_to_half2<0x4342>(ab) : codes_to_half2<0x4140>(ab);
+            const uint32_t b1 = (i & 1) ? codes_to_half2<0x4342>(cd) : codes_to_half2<0x4140>(cd);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int p = 0; p < NQ; ++p) mma16816(o[mt][4 * c + i], pf[mt][x][p], b0, b1);
+          }
+        }
+      }
+
+      __syncwarp();                      // every lane has read the stage
+      if (j + S < count) issue(j + S, stage);
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+
+    // ---- join the warps: each leaves its normalised output in its ring
+    float* mine = (float*)ring;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float sum = l[mt][hf];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = mt * 16 + hf * 8 + g;
+        if (t == 0) ml[warp][r] = make_float2(m[mt][hf], sum);
+        // NaN sums stay NaN; a row that saw no key gives 0
+        const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+        float out[E];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          out[i] = o[mt][i][2 * hf] * by * vref;
+          out[NT + i] = o[mt][i][2 * hf + 1] * by * vref;
+        }
+#pragma unroll
+        for (int d = 0; d < E; d += 4)
+          *reinterpret_cast<float4*>(mine + r * DH + E * t + d) =
+              make_float4(out[d], out[d + 1], out[d + 2], out[d + 3]);
+      }
+    }
+    __syncthreads();
+
+    const int64_t pair_last = pair_pos + w_pair - 1;
+    const int first_cta = (int)(pair_pos / share), last_cta = (int)(pair_last / share);
+    const bool whole = first_cta == last_cta;
+    float* part = a.part + (int64_t)(2 * blockIdx.x + (blockIdx.x == first_cta ? 1 : 0)) * (R * DH + 2 * R);
+    auto store = [&](int r, int d, float4 v, float top, float sum) {
+      const int rr = r_base + r;
+      const int64_t at = (q0 + rr / a.G) * a.Hq + h * a.G + rr % a.G;
+      T* dst = (T*)a.O + at * DH + d;
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(dst) = v;
+      } else {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+      }
+      if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - kOffset) * kLn2;
+    };
+    for (int i = threadIdx.x; i < rows * (DH / 4); i += kWarps * 32) {
+      const int r = i / (DH / 4), d = i % (DH / 4) * 4;
+      float2 x[kWarps];
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        x[w] = ml[w][r];
+        top = fmaxf(top, x[w].x);
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        x[w].y *= ex2(x[w].x - (top == -INFINITY ? 0.0f : top));
+        sum += x[w].y;
+      }
+      const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>((float*)(smem + w * Tile<DH>::kRing) + r * DH + d);
+        const float k = x[w].y * by;
+        v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+      }
+      if (whole) {
+        store(r, d, v, top, sum);
+      } else {
+        *reinterpret_cast<float4*>(part + r * DH + d) = v;
+        if (d == 0) *reinterpret_cast<float2*>(part + R * DH + 2 * r) = make_float2(top, sum);
+      }
+    }
+    if (!whole) {
+      // the last block to arrive joins the pair's parts in the blocks' order
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) is_last = atomicAdd(a.tickets + first_cta, 1) == last_cta - first_cta;
+      __syncthreads();
+      if (is_last) {
+        __threadfence();
+        const int64_t pitch = R * DH + 2 * R;
+        auto slot = [&](int c) { return a.part + (2 * (int64_t)c + (c == first_cta ? 1 : 0)) * pitch; };
+        for (int i = threadIdx.x; i < rows * (DH / 4); i += kWarps * 32) {
+          const int r = i / (DH / 4), d = i % (DH / 4) * 4;
+          float top = -INFINITY;
+          for (int c = first_cta; c <= last_cta; ++c)
+            top = fmaxf(top, __ldcg(slot(c) + R * DH + 2 * r));
+          float sum = 0.0f;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int c = first_cta; c <= last_cta; ++c) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(slot(c) + R * DH + 2 * r));
+            const float k = x.y * ex2(x.x - (top == -INFINITY ? 0.0f : top));
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(slot(c) + r * DH + d));
+            sum += k;
+            v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+          }
+          const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+          store(r, d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by), top, sum);
+        }
+      }
+    }
+    fence_proxy_async_smem();            // the ring's next writes are TMA's
+    __syncthreads();
+    pos = seg_end;
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+size_t part_floats(int R, int DH) { return (size_t)R * DH + 2 * R; }
+
+// Query rows of a pair: 32 where a warp's registers hold two row tiles.
+int pair_rows(const lime_kv_dims& D, int64_t rows_per_head) {
+  return D.dtype == LIME_BF16 && D.dh <= 64 && rows_per_head > 16 ? 32 : 16;
+}
+
+template <typename T, int DH, int MT>
+int launch(const lime_kv_dims& D, Args a, CUtensorMap mk, CUtensorMap mv, Plan* plan,
+           int64_t* prefix, cudaStream_t st) {
+  auto kernel = k_kv_attn<T, DH, MT>;
+  const size_t smem = kWarps * Tile<DH>::kRing + 1024;
+  static int per_sm[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LIME_ERR_CUDA;
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!per_sm[dev]) {
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kWarps * 32, smem) != cudaSuccess ||
+        n < 1)
+      return LIME_ERR_CUDA;
+    per_sm[dev] = n;
+  }
+  int grid = num_sms() * per_sm[dev];
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  int rc = launch_pdl(k_kv_plan, dim3(1), dim3(1024), 0, st, 1, a.B, a.off, a.total_q, a.lens,
+                      a.Hkv, a.G, (int64_t)a.max_blocks * a.block, 16 * MT, (int)Tile<DH>::TK, grid,
+                      plan, prefix, a.tickets, a.status);
+  if (rc) return rc;
+  return launch_pdl(kernel, dim3(grid), dim3(kWarps * 32), smem, st, 1, mk, mv, a);
 }
 
 }  // namespace
 
 size_t kv_ws_bytes(const lime_kv_dims& D, int64_t B, int64_t total_q) {
-  return (size_t)B * 8;  // ranks of the requests' blocks
+  const size_t ranks = (size_t)B * 8;  // of the requests' blocks (reserve, release)
+  if (total_q == 0) return ranks;
+  const size_t attn = 256 + ((size_t)(B + 1) * 8 + 255) / 256 * 256 + kMaxCtas * 4 +
+                      2 * kMaxCtas * part_floats(D.dh <= 64 ? 32 : 16, D.dh) * 4;
+  return attn > ranks ? attn : ranks;
 }
 
 int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, const int64_t* off,
                  int64_t total_q, const int32_t* table, const int32_t* lens, const int8_t* kc,
                  const int8_t* vc, const float* scale, float sm_scale, bool causal, void* O,
                  float* lse, void* ws, unsigned* status, cudaStream_t st) {
-  if (D.dtype == LIME_BF16)
-    launch<bf16>(D, B, Q, ldq, off, total_q, table, lens, kc, vc, scale, sm_scale, causal, O, lse,
-                 status, st);
-  else
-    launch<float>(D, B, Q, ldq, off, total_q, table, lens, kc, vc, scale, sm_scale, causal, O, lse,
-                  status, st);
-  return LIME_OK;
+  const int G = D.Hq / D.Hkv;
+  const int R = pair_rows(D, ceil_div(total_q, B) * G);
+  const int TK = D.dh == 128 ? 32 : 64;
+  char* p = (char*)ws;
+  Plan* plan = (Plan*)p;
+  int64_t* prefix = (int64_t*)(p + 256);
+  p += 256 + ((size_t)(B + 1) * 8 + 255) / 256 * 256;
+
+  CUtensorMap mk, mv;
+  const int box = D.block < TK ? D.block : TK;
+  if (!make_tmap_kv(&mk, kc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh) ||
+      !make_tmap_kv(&mv, vc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh))
+    return LIME_ERR_CUDA;
+  Args a = {};
+  a.Q = Q, a.ldq = ldq, a.off = off, a.table = table, a.lens = lens;
+  a.scale = (const float2*)scale;
+  a.plan = plan, a.prefix = prefix, a.tickets = (int*)p, a.part = (float*)(p + kMaxCtas * 4);
+  a.O = O, a.lse = lse, a.status = status;
+  a.B = B, a.total_q = total_q, a.n_blocks = D.n_blocks;
+  a.Hq = D.Hq, a.Hkv = D.Hkv, a.G = G, a.block = D.block, a.max_blocks = D.max_blocks;
+  a.scale_log2 = fabsf(sm_scale) * kLog2e, a.negative = sm_scale < 0.0f, a.causal = causal;
+#define RUN(T, DH, MT) return launch<T, DH, MT>(D, a, mk, mv, plan, prefix, st)
+  if (D.dtype == LIME_BF16) {
+    if (D.dh == 16) { if (R == 32) RUN(bf16, 16, 2); RUN(bf16, 16, 1); }
+    if (D.dh == 32) { if (R == 32) RUN(bf16, 32, 2); RUN(bf16, 32, 1); }
+    if (D.dh == 64) { if (R == 32) RUN(bf16, 64, 2); RUN(bf16, 64, 1); }
+    RUN(bf16, 128, 1);
+  }
+  if (D.dh == 16) RUN(float, 16, 1);
+  if (D.dh == 32) RUN(float, 32, 1);
+  if (D.dh == 64) RUN(float, 64, 1);
+  RUN(float, 128, 1);
+#undef RUN
 }
 
 }  // namespace lime

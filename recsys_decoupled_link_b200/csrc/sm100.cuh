@@ -321,6 +321,12 @@ bool make_tmap_2d_u8_plain(CUtensorMap* map, const void* base, uint64_t inner, u
 bool make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                       uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// Host: a pool of `tiles` contiguous tiles of tile_bytes each (a multiple of
+// 128), as rows of 128 bytes with 128-byte swizzle; a box is box_bytes of one
+// tile.  Coordinates: (0, row of 128 bytes, tile).
+bool make_tmap_kv(CUtensorMap* map, const void* base, uint64_t tile_bytes, uint64_t tiles,
+                  uint32_t box_bytes);
+
 // Host: number of SMs of the current device (cached per device).
 int num_sms();
 

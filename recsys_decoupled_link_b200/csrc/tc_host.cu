@@ -101,6 +101,20 @@ bool make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_kv(CUtensorMap* map, const void* base, uint64_t tile_bytes, uint64_t tiles,
+                  uint32_t box_bytes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {128, tile_bytes / 128, tiles};
+  cuuint64_t strides[2] = {128, tile_bytes};
+  cuuint32_t box[3] = {128, box_bytes / 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 int num_sms() {
   static int cached[64] = {0};
   int dev = 0;

@@ -175,7 +175,7 @@ def test_oracle_attention_is_torch_attention():
             mask = mask.tril(n - m)
         ref = torch.nn.functional.scaled_dot_product_attention(
             torch.tensor(q).transpose(0, 1), flat(k, 0), flat(v, 1), attn_mask=mask)
-        got, lse, A, S = K.attention(q, [m], table, [n], k, v, scale, bs, dh ** -0.5, causal)
+        got, lse, A, S, V = K.attention(q, [m], table, [n], k, v, scale, bs, dh ** -0.5, causal)
         np.testing.assert_allclose(got, ref.transpose(0, 1).numpy(), rtol=1e-12, atol=1e-12)
         s = torch.tensor(q).transpose(0, 1) @ flat(k, 0).transpose(1, 2) * dh ** -0.5
         s = s.masked_fill(~mask, -np.inf).logsumexp(-1).T.numpy()
@@ -186,7 +186,7 @@ def test_oracle_attention_is_torch_attention():
 def test_oracle_attention_without_keys():
     q = np.ones((4, 1, 16))
     k = np.ones((1, 1, 16, 16), dtype=np.int8)
-    O, lse, _, _ = K.attention(q, [3, 1], [[0], [0]], [2, 0], k, k, np.ones((1, 1, 2)), 16, 1.0, True)
+    O, lse, *_ = K.attention(q, [3, 1], [[0], [0]], [2, 0], k, k, np.ones((1, 1, 2)), 16, 1.0, True)
     assert (O[0] == 0).all() and np.isneginf(lse[0]).all()          # 3 queries, 2 rows: none seen
     np.testing.assert_allclose(O[1], 1.0)
     assert (O[3] == 0).all() and np.isneginf(lse[3]).all()          # an empty history
