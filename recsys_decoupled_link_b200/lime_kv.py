@@ -14,8 +14,8 @@ from typing import Optional
 
 import torch
 
-from .lime import (LIME_BF16, LIME_ERR_SHAPE, LIME_F32, LimeError, _check, _lib, _ptr, _stream,
-                   lime_get_status, lime_workspace_init)
+from .lime import (LIME_BF16, LIME_ERR_SHAPE, LIME_F32, LimeError, _lib, lime_get_status,
+                   lime_workspace_init)
 
 LIME_FLAG_BAD_BLOCK, LIME_FLAG_NO_BLOCKS, LIME_FLAG_NONFINITE = 8, 16, 32
 
@@ -65,109 +65,165 @@ class KvWorkspace:
         if n == 0:
             raise LimeError("lime_kv_workspace_bytes", LIME_ERR_SHAPE)
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
-        self.nbytes = n
+        self.nbytes, self.address = n, self.buf.data_ptr()
+        self.device = self.buf.get_device()
         lime_workspace_init(self, stream=stream)
 
     @property
     def ptr(self):
-        return ctypes.c_void_p(self.buf.data_ptr())
+        return ctypes.c_void_p(self.address)
+
+
+_i8, _i32, _i64, _f32 = torch.int8, torch.int32, torch.int64, torch.float32
 
 
 def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
-def _want(name: str, t: torch.Tensor, dtype, shape):
-    """A tensor's type, device and shape (-1: any size), checked before its pointer is passed."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if t.get_device() != _device():
-        raise ValueError(f"{name}: liblime takes tensors of the current device")
-    if t.dim() != len(shape) or any(w not in (-1, g) for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _rows(name: str, t: torch.Tensor, dims: lime_kv_dims, heads: int):
-    """Pointer and row pitch of packed rows [n, heads, dh]; rows may be strided."""
-    _want(name, t, torch.bfloat16 if dims.dtype == LIME_BF16 else torch.float32,
-          (-1, heads, dims.dh))
-    if (heads > 1 and t.stride(1) != dims.dh) or t.stride(2) != 1:
+def _refuse(dev: int, ws, *tensors):
+    """Raises for the first tensor (name, tensor, dtype, shape with -1 for any size, "strided"
+    where its rows may be) that is not what a call takes, or for a workspace elsewhere.  The calls test all of them in one expression first, and come here only to
+    name the one at fault: a call's checks are much of what a small call costs on the host."""
+    for name, t, dtype, shape, *strided in tensors:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+        if t.dim() != len(shape) or any(w not in (-1, g) for w, g in zip(shape, t.shape)):
+            raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: liblime takes tensors of the current device")
+        if not strided and not t.is_contiguous():
+            raise ValueError(f"{name}: liblime takes contiguous tensors")
+    if ws is not None and ws.device != dev:
+        raise ValueError("workspace: liblime takes tensors of the current device")
+
+
+def _row_dtype(dims):
+    return torch.bfloat16 if dims.dtype == LIME_BF16 else torch.float32
+
+
+def _pitch(name: str, t: torch.Tensor, heads: int, dh: int) -> int:
+    """Elements between the rows of t [n, heads, dh], whose heads have to be contiguous."""
+    ld, sh, sd = t.stride()
+    if sd != 1 or (sh != dh and heads > 1):
         raise ValueError(f"{name}: the heads of a row have to be contiguous")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dims.dh)
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return ld if t.shape[0] > 1 else max(ld, heads * dh)
 
 
-def _pool(dims: lime_kv_dims, k_cache, v_cache, scale):
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _want(name, t, torch.int8, (dims.n_blocks, dims.Hkv, dims.block, dims.dh))
-    _want("scale", scale, torch.float32, (dims.n_blocks, dims.Hkv, 2))
+def _check_pool(dims, dev, k_cache, v_cache, scale):
+    shape = (dims.n_blocks, dims.Hkv, dims.block, dims.dh)
+    if not (k_cache.dtype is _i8 and v_cache.dtype is _i8 and scale.dtype is _f32
+            and k_cache.shape == shape and v_cache.shape == shape
+            and scale.shape == (shape[0], shape[1], 2) and k_cache.get_device() == dev
+            and v_cache.get_device() == dev and scale.get_device() == dev
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and scale.is_contiguous()):
+        _refuse(dev, None, ("k_cache", k_cache, _i8, shape), ("v_cache", v_cache, _i8, shape),
+                ("scale", scale, _f32, (shape[0], shape[1], 2)))
 
 
 def lime_kv_reserve(dims, lens, new_offsets, block_table, free_blocks, n_free, lens_out,
                     n_free_out, slot_map, ws: KvWorkspace, stream=None):
-    B = lens.shape[0]
-    for name, t, dtype, shape in (
-            ("lens", lens, torch.int32, (B,)), ("new_offsets", new_offsets, torch.int64, (B + 1,)),
-            ("block_table", block_table, torch.int32, (B, dims.max_blocks)),
-            ("free_blocks", free_blocks, torch.int32, (-1,)),
-            ("n_free", n_free, torch.int32, (1,)), ("lens_out", lens_out, torch.int32, (B,)),
-            ("n_free_out", n_free_out, torch.int32, (1,)),
-            ("slot_map", slot_map, torch.int64, (-1,))):
-        _want(name, t, dtype, shape)
-    _check("lime_kv_reserve", _lib.lime_kv_reserve(
-        ctypes.byref(dims), B, _ptr(lens), _ptr(new_offsets), slot_map.shape[0],
-        _ptr(block_table), _ptr(free_blocks), free_blocks.shape[0], _ptr(n_free), _ptr(lens_out),
-        _ptr(n_free_out), _ptr(slot_map), ws.ptr, ws.nbytes, _stream(stream)))
+    B, dev = lens.shape[0], _device()
+    n, cap = slot_map.shape[0], free_blocks.shape[0]
+    if not (lens.dtype is _i32 and new_offsets.dtype is _i64 and block_table.dtype is _i32
+            and free_blocks.dtype is _i32 and n_free.dtype is _i32 and lens_out.dtype is _i32
+            and n_free_out.dtype is _i32 and slot_map.dtype is _i64
+            and lens.shape == (B,) and new_offsets.shape == (B + 1,)
+            and block_table.shape == (B, dims.max_blocks) and free_blocks.shape == (cap,)
+            and n_free.shape == (1,) and lens_out.shape == (B,) and n_free_out.shape == (1,)
+            and slot_map.shape == (n,)
+            and lens.get_device() == dev and new_offsets.get_device() == dev
+            and block_table.get_device() == dev and free_blocks.get_device() == dev
+            and n_free.get_device() == dev and lens_out.get_device() == dev
+            and n_free_out.get_device() == dev and slot_map.get_device() == dev
+            and lens.is_contiguous() and new_offsets.is_contiguous()
+            and block_table.is_contiguous() and free_blocks.is_contiguous()
+            and lens_out.is_contiguous() and slot_map.is_contiguous() and ws.device == dev):
+        _refuse(dev, ws, ("lens", lens, _i32, (B,)), ("new_offsets", new_offsets, _i64, (B + 1,)),
+                ("block_table", block_table, _i32, (B, dims.max_blocks)),
+                ("free_blocks", free_blocks, _i32, (-1,)), ("n_free", n_free, _i32, (1,)),
+                ("lens_out", lens_out, _i32, (B,)), ("n_free_out", n_free_out, _i32, (1,)),
+                ("slot_map", slot_map, _i64, (-1,)))
+    rc = _lib.lime_kv_reserve(
+        ctypes.byref(dims), B, lens.data_ptr(), new_offsets.data_ptr(), n, block_table.data_ptr(),
+        free_blocks.data_ptr(), cap, n_free.data_ptr(), lens_out.data_ptr(),
+        n_free_out.data_ptr(), slot_map.data_ptr(), ws.address, ws.nbytes, _raw_stream(stream, dev))
+    if rc:
+        raise LimeError("lime_kv_reserve", rc)
 
 
 def lime_kv_release(dims, lens, keep: Optional[torch.Tensor], block_table, free_blocks, n_free,
                     lens_out, n_free_out, ws: KvWorkspace, stream=None):
-    B = lens.shape[0]
-    for name, t, dtype, shape in (
-            ("lens", lens, torch.int32, (B,)),
-            ("block_table", block_table, torch.int32, (B, dims.max_blocks)),
-            ("free_blocks", free_blocks, torch.int32, (-1,)),
-            ("n_free", n_free, torch.int32, (1,)), ("lens_out", lens_out, torch.int32, (B,)),
-            ("n_free_out", n_free_out, torch.int32, (1,))):
-        _want(name, t, dtype, shape)
-    if keep is not None:
-        _want("keep", keep, torch.int32, (B,))
-    _check("lime_kv_release", _lib.lime_kv_release(
-        ctypes.byref(dims), B, _ptr(lens), _ptr(keep), _ptr(block_table), _ptr(free_blocks),
-        free_blocks.shape[0], _ptr(n_free), _ptr(lens_out), _ptr(n_free_out), ws.ptr, ws.nbytes,
-        _stream(stream)))
+    B, dev = lens.shape[0], _device()
+    _refuse(dev, ws, ("lens", lens, _i32, (B,)), ("keep", keep, _i32, (B,)),
+            ("block_table", block_table, _i32, (B, dims.max_blocks)),
+            ("free_blocks", free_blocks, _i32, (-1,)), ("n_free", n_free, _i32, (1,)),
+            ("lens_out", lens_out, _i32, (B,)), ("n_free_out", n_free_out, _i32, (1,)))
+    rc = _lib.lime_kv_release(
+        ctypes.byref(dims), B, lens.data_ptr(), None if keep is None else keep.data_ptr(),
+        block_table.data_ptr(), free_blocks.data_ptr(), free_blocks.shape[0], n_free.data_ptr(),
+        lens_out.data_ptr(), n_free_out.data_ptr(), ws.address, ws.nbytes,
+        _raw_stream(stream, dev))
+    if rc:
+        raise LimeError("lime_kv_release", rc)
 
 
 def lime_kv_append(dims, K, V, slot_map, k_cache, v_cache, scale, ws: KvWorkspace, stream=None):
     """K, V [n, Hkv, dh] with any row pitch; slot_map int64 [n]."""
-    k, ldk = _rows("K", K, dims, dims.Hkv)
-    v, ldv = _rows("V", V, dims, dims.Hkv)
-    _want("slot_map", slot_map, torch.int64, (K.shape[0],))
-    _want("V", V, K.dtype, K.shape)
-    _pool(dims, k_cache, v_cache, scale)
-    _check("lime_kv_append", _lib.lime_kv_append(
-        ctypes.byref(dims), k, ldk, v, ldv, K.shape[0], _ptr(slot_map), _ptr(k_cache),
-        _ptr(v_cache), _ptr(scale), ws.ptr, ws.nbytes, _stream(stream)))
+    n, dev, dt = slot_map.shape[0], _device(), _row_dtype(dims)
+    shape = (n, dims.Hkv, dims.dh)
+    if not (K.dtype is dt and V.dtype is dt and slot_map.dtype is _i64 and K.shape == shape
+            and V.shape == shape and slot_map.shape == (n,) and K.get_device() == dev
+            and V.get_device() == dev and slot_map.get_device() == dev
+            and slot_map.is_contiguous() and ws.device == dev):
+        _refuse(dev, ws, ("slot_map", slot_map, _i64, (-1,)), ("K", K, dt, shape, "strided"),
+                ("V", V, dt, shape, "strided"))
+    ldk, ldv = _pitch("K", K, shape[1], shape[2]), _pitch("V", V, shape[1], shape[2])
+    _check_pool(dims, dev, k_cache, v_cache, scale)
+    rc = _lib.lime_kv_append(
+        ctypes.byref(dims), K.data_ptr(), ldk, V.data_ptr(), ldv, n, slot_map.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), scale.data_ptr(), ws.address, ws.nbytes,
+        _raw_stream(stream, dev))
+    if rc:
+        raise LimeError("lime_kv_append", rc)
 
 
 def lime_kv_attention(dims, Q, q_offsets, block_table, lens, k_cache, v_cache, scale, O, lse,
                       ws: KvWorkspace, sm_scale: Optional[float] = None, causal: bool = False,
                       stream=None):
     """Q [n, Hq, dh] with any row pitch; lse fp32 [n, Hq] or None; sm_scale 1/sqrt(dh) if None."""
-    B = lens.shape[0]
-    q, ldq = _rows("Q", Q, dims, dims.Hq)
-    _want("q_offsets", q_offsets, torch.int64, (B + 1,))
-    _want("block_table", block_table, torch.int32, (B, dims.max_blocks))
-    _want("lens", lens, torch.int32, (B,))
-    _want("O", O, Q.dtype, Q.shape)
-    if lse is not None:
-        _want("lse", lse, torch.float32, Q.shape[:2])
-    _pool(dims, k_cache, v_cache, scale)
-    sm = 1.0 / math.sqrt(dims.dh) if sm_scale is None else sm_scale
-    _check("lime_kv_attention", _lib.lime_kv_attention(
-        ctypes.byref(dims), B, q, ldq, _ptr(q_offsets), Q.shape[0], _ptr(block_table), _ptr(lens),
-        _ptr(k_cache), _ptr(v_cache), _ptr(scale), sm, int(causal), _ptr(O), _ptr(lse), ws.ptr,
-        ws.nbytes, _stream(stream)))
+    B, n, dev, dt = lens.shape[0], Q.shape[0], _device(), _row_dtype(dims)
+    shape = (n, dims.Hq, dims.dh)
+    if not (Q.dtype is dt and O.dtype is dt and q_offsets.dtype is _i64
+            and block_table.dtype is _i32 and lens.dtype is _i32 and Q.shape == shape
+            and O.shape == shape and q_offsets.shape == (B + 1,)
+            and block_table.shape == (B, dims.max_blocks) and lens.shape == (B,)
+            and Q.get_device() == dev and O.get_device() == dev and q_offsets.get_device() == dev
+            and block_table.get_device() == dev and lens.get_device() == dev
+            and O.is_contiguous() and q_offsets.is_contiguous() and block_table.is_contiguous()
+            and lens.is_contiguous() and ws.device == dev
+            and (lse is None or (lse.dtype is _f32 and lse.shape == shape[:2]
+                                 and lse.get_device() == dev and lse.is_contiguous()))):
+        _refuse(dev, ws, ("q_offsets", q_offsets, _i64, (B + 1,)),
+                ("block_table", block_table, _i32, (B, dims.max_blocks)),
+                ("lens", lens, _i32, (B,)), ("O", O, dt, shape), ("lse", lse, _f32, shape[:2]),
+                ("Q", Q, dt, shape, "strided"))
+    ldq = _pitch("Q", Q, shape[1], shape[2])
+    _check_pool(dims, dev, k_cache, v_cache, scale)
+    rc = _lib.lime_kv_attention(
+        ctypes.byref(dims), B, Q.data_ptr(), ldq, q_offsets.data_ptr(), n, block_table.data_ptr(),
+        lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), scale.data_ptr(),
+        1.0 / math.sqrt(dims.dh) if sm_scale is None else sm_scale, 1 if causal else 0,
+        O.data_ptr(), None if lse is None else lse.data_ptr(), ws.address, ws.nbytes,
+        _raw_stream(stream, dev))
+    if rc:
+        raise LimeError("lime_kv_attention", rc)
 
 
 class HistoryCache:
