@@ -56,9 +56,15 @@ typedef struct {
 } lime_kv_dims;
 
 /* Bytes of device workspace for calls with up to B requests and total_q query
- * rows (256-byte aligned, prepared once by lime_workspace_init); 0 for
+ * rows (256-byte aligned, prepared once by lime_kv_workspace_init); 0 for
  * unsupported dims. */
 size_t lime_kv_workspace_bytes(const lime_kv_dims* dims, int64_t B, int64_t total_q);
+
+/* Clears the workspace's status word and the counters that the calls leave at
+ * zero (asynchronous on stream).  Once before the first call, and again after
+ * a call that set LIME_FLAG_TIMEOUT.  LIME_ERR_ARG for a workspace smaller
+ * than any lime_kv_workspace_bytes. */
+int lime_kv_workspace_init(void* workspace, size_t bytes, cudaStream_t stream);
 
 /* Block table and slot map of new rows, built from the requests' lengths.
  *   lens          device int32 [B]      rows each request holds

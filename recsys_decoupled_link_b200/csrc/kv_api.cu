@@ -62,7 +62,11 @@ int check_ws(void* ws, size_t bytes, const lime_kv_dims* D, int64_t B, int64_t t
 }
 
 unsigned* status_of(void* ws) { return (unsigned*)ws; }
-void* scratch_of(void* ws) { return (char*)ws + kStatusBytes; }
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+// status word, tickets (zero between calls), scratch
+int* tickets_of(void* ws) { return (int*)((char*)ws + kStatusBytes); }
+size_t head_bytes() { return kStatusBytes + round256(kv_ticket_bytes()); }
+void* scratch_of(void* ws) { return (char*)ws + head_bytes(); }
 
 int launch_status(const char* what) {
   cudaError_t e = cudaGetLastError();
@@ -79,7 +83,14 @@ extern "C" {
 
 size_t lime_kv_workspace_bytes(const lime_kv_dims* dims, int64_t B, int64_t total_q) {
   if (check_dims(dims) != LIME_OK || bad_count(B) || bad_count(total_q)) return 0;
-  return kStatusBytes + ((kv_ws_bytes(*dims, B, total_q) + 255) & ~(size_t)255);
+  const size_t ranks = (size_t)B * 8, attn = kv_attention_ws_bytes(*dims, B, total_q);
+  return head_bytes() + round256(attn > ranks ? attn : ranks);
+}
+
+int lime_kv_workspace_init(void* workspace, size_t bytes, cudaStream_t stream) {
+  if (!workspace || bytes < head_bytes() || !aligned(workspace, 256)) return LIME_ERR_ARG;
+  return cudaMemsetAsync(workspace, 0, head_bytes(), stream) == cudaSuccess ? LIME_OK
+                                                                            : LIME_ERR_CUDA;
 }
 
 int lime_kv_reserve(const lime_kv_dims* dims, int64_t B, const int32_t* lens,
@@ -214,7 +225,7 @@ int lime_kv_attention(const lime_kv_dims* dims, int64_t B, const void* Q, int64_
   if (clash(s, 3, 10)) return LIME_ERR_ALIAS;
   if ((rc = kv_attention(*dims, B, Q, ldq, q_offsets, total_q, block_table, lens, k_cache, v_cache,
                          scale, sm_scale, causal != 0, O, lse, scratch_of(workspace),
-                         status_of(workspace), stream)))
+                         tickets_of(workspace), status_of(workspace), stream)))
     return rc;
   return launch_status("lime_kv_attention");
 }

@@ -2,7 +2,7 @@
 //
 // A pair is one (request, kv head, tile of R query rows).  Its cached rows are
 // cut into tiles of TK keys; all pairs' tiles, laid end to end, are divided
-// evenly over the thread blocks (k_kv_plan), so that ragged requests load
+// evenly over the thread blocks, so that ragged requests load
 // every SM alike.  A block's share of one pair is a segment; the block's warps
 // take the segment's tiles in turn, each with its own softmax state and its own
 // ring of TMA stages, and join their states at the segment's end.  A pair cut
@@ -31,24 +31,26 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxCtas = 640;       // most blocks of the persistent grid
-constexpr int kPairCost = 4;        // a pair's fixed cost, in tiles
+constexpr int kPairCost = 12;       // a pair's fixed cost, in tiles
+constexpr int kJoin = 8;            // parts of a cut pair read at a time
+constexpr int kLeastTiles = 16;     // fewest tiles worth a block of their own
 constexpr float kOffset = 14.0f;    // probabilities enter fp16 times 2^14
+constexpr float kSlack = 1.5f;      // log2 by which a row's reference may lag its maximum
 constexpr float kTiny = 1e-37f;     // least factor of a score: -inf times 0 would be NaN
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Per head dim: keys of a warp's tile and stages of its ring.
+// Per head dim: keys of a warp's tile (one ring stage), keys of one softmax
+// step, stages of the ring.
 template <int DH> struct Tile {
   static constexpr int TK = DH == 128 ? 32 : 64;
-  static constexpr int kStages = DH == 128 ? 3 : DH == 64 ? 3 : 4;
+  static constexpr int SK = DH <= 32 ? 64 : 32;
+  static constexpr int kStages = DH <= 32 ? 3 : DH == 64 ? 2 : 2;
   static constexpr int kBytes = TK * DH;             // keys (or values) of a tile
   static constexpr int kRing = kStages * 2 * kBytes; // per warp
 };
 
-struct Plan {
-  int64_t total;  // weight of all pairs: tiles plus kPairCost each
-  int64_t share;  // weight of one block
-};
+constexpr int kInlineRequests = 2048;  // most requests whose weights every block sums itself
 
 struct Args {
   const void* Q;
@@ -57,15 +59,17 @@ struct Args {
   const int32_t* table;
   const int32_t* lens;
   const float2* scale;
-  const Plan* plan;
-  const int64_t* prefix;  // [B + 1] weight before each request
-  int* tickets;           // [grid]
+  const int64_t* prefix;  // [B + 2] weight before each request, then the
+                          // number of pairs (NULL: summed by every block)
+  int* tickets;           // [grid] zero between calls
   float* part;            // [2 * grid] partial results
   void* O;
   float* lse;
   unsigned* status;
   int64_t B, total_q, n_blocks;
-  int Hq, Hkv, G, block, max_blocks;
+  int Hq, Hkv, G, max_blocks;
+  int log_block;
+  int log_g;         // of G, or -1 where it is no power of two
   float scale_log2;  // |sm_scale| log2 e
   bool negative;     // sm_scale < 0
   bool causal;
@@ -77,29 +81,58 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// x / y, in 32 bits where they suffice (a 64-bit division takes most of a
+// microsecond of a segment's start).
+__device__ __forceinline__ int64_t div_by(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
+
 // ------------------------------------------------------------------- plan
 
-// Prefix sums of the requests' weights, the blocks' share and cleared tickets.
+// Pairs of a request, and their weight: each its tiles and kPairCost.
+__device__ __forceinline__ int64_t pairs_of(int64_t rows, int Hkv, int G, int R) {
+  return ceil_div(rows * G, R) * Hkv;
+}
+__device__ __forceinline__ int64_t weight_of(int64_t pairs, int n, int TK) {
+  return pairs * (ceil_div(n, TK) + kPairCost);
+}
+
+// A block's share of all weight.  Where there are more blocks than pairs, one
+// below kLeastTiles would only add joins, and one above the pairs' mean would
+// put two of them into one block.
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t pairs, int grid) {
+  const int64_t share = div_by(total + grid - 1, grid), mean = div_by(total + pairs - 1, pairs);
+  int64_t least = kPairCost + kLeastTiles;
+  if (least > mean) least = mean;
+  return share > least ? share : least;
+}
+
+// Prefix sums of the requests' weights, where there are too many requests for
+// every block to sum them.
 __global__ void __launch_bounds__(1024)
     k_kv_plan(int64_t B, const int64_t* off, int64_t total_q, const int32_t* lens, int Hkv, int G,
-              int64_t most, int R, int TK, int grid, Plan* plan, int64_t* prefix, int* tickets,
-              unsigned* status) {
+              int64_t most, int R, int TK, int64_t* prefix, unsigned* status) {
   __shared__ int64_t part[32];
+  __shared__ unsigned long long all_pairs;
+  if (threadIdx.x == 0) all_pairs = 0;
+  __syncthreads();
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < grid; i += blockDim.x) tickets[i] = 0;
   const int64_t per = ceil_div(B, 1024);
   const int64_t u0 = per * threadIdx.x, u1 = u0 + per < B ? u0 + per : B;
-  int64_t sum = 0;
+  int64_t sum = 0, pairs = 0;
   for (int64_t u = u0; u < u1; ++u) {
     int64_t a, b;
     user_range(off, u, B, total_q, &a, &b, status);
-    const int n = kv_len(lens, u, most, status);
-    const int64_t w = ceil_div((b - a) * G, R) * Hkv * (ceil_div(n, TK) + kPairCost);
+    const int64_t p = pairs_of(b - a, Hkv, G, R);
+    const int64_t w = weight_of(p, kv_len(lens, u, most, status), TK);
     prefix[u] = w;
     sum += w;
+    pairs += p;
   }
+  if (pairs) atomicAdd(&all_pairs, (unsigned long long)pairs);
   int64_t x = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -125,12 +158,8 @@ __global__ void __launch_bounds__(1024)
     at += w;
   }
   if (threadIdx.x == 0) {
-    const int64_t all = part[31];
-    prefix[B] = all;
-    plan->total = all;
-    // a share below one tile per warp would only add joins
-    const int64_t share = ceil_div(all, grid), least = kPairCost + kWarps;
-    plan->share = share > least ? share : least;
+    prefix[B] = part[31];
+    prefix[B + 1] = (int64_t)all_pairs;
   }
 }
 
@@ -153,11 +182,44 @@ __device__ __forceinline__ int64_t find_request(const int64_t* prefix, int64_t B
 // -------------------------------------------------------------- fragments
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same onto zero.
+__device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Two fp32 values to an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -165,8 +227,9 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The same, the largest finite fp16 in place of an overflow (a probability's
-// exponent is off by more than 2 once scores pass 2^25).
+// The same, the largest finite fp16 in place of an overflow: a probability is at
+// most 2^(kOffset + kSlack), unless scores beyond 2^22 cost its exponent half a
+// unit.
 __device__ __forceinline__ uint32_t half2_sat(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -186,6 +249,11 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
 // Byte offset inside a tile, through the 128-byte swizzle the TMA applies.
 __device__ __forceinline__ uint32_t swz(uint32_t off) { return off ^ (((off >> 7) & 7u) << 4); }
 
+// swz(lane | c) from at = swz(lane), where lane and the constant c share no bit.
+__device__ __forceinline__ uint32_t swz_at(uint32_t at, uint32_t c) {
+  return (at ^ (((c >> 7) & 7u) << 4)) + c;
+}
+
 // Which of 16 keys a fragment's columns stand for.  Column c of the first
 // (second) 8-key product is key col(c) (col(c) + odd): lane t of a quad then
 // holds in both products the scores, and as value rows the codes, of keys
@@ -203,34 +271,39 @@ template <int DH> struct KeyMap {
   __device__ static __forceinline__ int key(int t, int i) { return col(2 * t + (i & 1)) + (i >> 1) * odd; }
 };
 
+// BYTES of shared memory into words.
 template <int BYTES>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
+__device__ __forceinline__ void lds(const uint8_t* p, uint32_t* w) {
   if constexpr (BYTES == 16) {
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr)
-                 : "memory");
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   } else if constexpr (BYTES == 8) {
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
   } else if constexpr (BYTES == 4) {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
-    asm volatile("{.reg .b16 x; ld.shared.b16 x, [%1]; cvt.u32.u16 %0, x;}"
-                 : "=r"(w[0])
-                 : "r"(addr)
-                 : "memory");
+    w[0] = *reinterpret_cast<const uint16_t*>(p);
   }
 }
 
 // ----------------------------------------------------------------- kernel
 
+// Blocks an SM holds, by registers.
 template <typename T, int DH, int MT>
-__global__ void __launch_bounds__(kWarps * 32)
+constexpr int min_blocks() {
+  return DH <= 32 ? (MT == 2 ? 2 : 4) : DH == 64 ? (MT == 2 ? 2 : 3) : (sizeof(T) == 2 ? 3 : 2);
+}
+
+// ONE: a softmax step's keys lie in one block (block >= SK), under one scale.
+template <typename T, int DH, int MT, bool ONE>
+__global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     k_kv_attn(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
               const Args a) {
   constexpr bool kSplit = sizeof(T) == 4;  // fp32 rows: operands as two fp16 terms
   constexpr int NQ = kSplit ? 2 : 1;
-  constexpr int TK = Tile<DH>::TK, S = Tile<DH>::kStages, NG = TK / 16;
+  constexpr int TK = Tile<DH>::TK, SK = Tile<DH>::SK, S = Tile<DH>::kStages, NG = SK / 16;
+  constexpr int NC = ONE ? 1 : NG;         // scales of a step
   constexpr int R = 16 * MT;
   constexpr int KS = DH / 16;              // k-steps of the score product
   constexpr int NT = DH / 8;               // 8-dim tiles of the output
@@ -242,12 +315,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   __shared__ uint64_t full[kWarps][S];
   __shared__ float2 ml[kWarps][R];
   __shared__ int abort_flag, is_last;
-  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ int64_t warp_sum[kWarps], warp_pairs[kWarps], found[2];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1,024-byte aligned: the swizzle's period
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * Tile<DH>::kRing;
-  const uint32_t ring_u32 = smem_u32(ring);
   if (threadIdx.x == 0) {
     abort_flag = 0;
     prefetch_tmap(&map_k);
@@ -260,123 +333,147 @@ __global__ void __launch_bounds__(kWarps * 32)
   pdl_launch();
   pdl_wait();
 
-  const int64_t share = a.plan->share, total = a.plan->total;
+  // where this block's share begins: request u, whose weights begin at before
+  const int bs = 1 << a.log_block;
+  const int64_t most = (int64_t)a.max_blocks << a.log_block;
+  int64_t u, before, total, share;
+  if (a.prefix) {
+    total = a.prefix[a.B];
+    if (total == 0) return;
+    share = share_of(total, a.prefix[a.B + 1], gridDim.x);
+    const int64_t at = share * blockIdx.x;
+    if (at >= total) return;
+    u = find_request(a.prefix, a.B, at);
+    before = a.prefix[u];
+  } else {
+    const int per = (int)ceil_div(a.B, kWarps * 32);
+    const int64_t u0 = (int64_t)per * threadIdx.x, u1 = u0 + per < a.B ? u0 + per : a.B;
+    int64_t sum = 0, count = 0;
+    for (int64_t v = u0; v < u1; ++v) {
+      int64_t x, y;
+      user_range(a.off, v, a.B, a.total_q, &x, &y, a.status);
+      const int64_t p = pairs_of(y - x, a.Hkv, a.G, R);
+      sum += weight_of(p, kv_len(a.lens, v, most, a.status), TK);
+      count += p;
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+      count += __shfl_xor_sync(0xffffffffu, count, o);
+    }
+    if (lane == 31) warp_sum[warp] = x, warp_pairs[warp] = count;
+    __syncthreads();
+    total = 0;
+    int64_t from = x - sum, pairs = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) from += warp_sum[w];
+      total += warp_sum[w];
+      pairs += warp_pairs[w];
+    }
+    if (total == 0) return;
+    share = share_of(total, pairs, gridDim.x);
+    const int64_t at = share * blockIdx.x;
+    if (at >= total) return;
+    if (from <= at && at < from + sum) {
+      int64_t v = u0;
+      for (;; ++v) {
+        int64_t p, q;
+        user_range(a.off, v, a.B, a.total_q, &p, &q, a.status);
+        const int64_t w = weight_of(pairs_of(q - p, a.Hkv, a.G, R), kv_len(a.lens, v, most, a.status), TK);
+        if (at < from + w) break;
+        from += w;
+      }
+      found[0] = v;
+      found[1] = from;
+    }
+    __syncthreads();
+    u = found[0];
+    before = found[1];
+  }
   int64_t pos = share * blockIdx.x;
   const int64_t pos_end = pos + share < total ? pos + share : total;
-  if (pos >= pos_end) return;
-  int64_t u = find_request(a.prefix, a.B, pos);
 
-  const int bs = a.block;
   const int nb = bs >= TK ? 1 : TK / bs;   // blocks of a tile
   const int box_rows = bs >= TK ? TK : bs;
   const uint32_t box_bytes = (uint32_t)box_rows * DH;
   const int batch = 32 / nb;               // tiles whose table entries a warp holds
 
-  // byte offsets of this lane's reads inside a 16-key group (the swizzle
-  // depends on the group only through whole 1024-byte rows and a constant)
-  const int kcol = Map::col(g);
+  // this lane's reads: key rows, and value rows of the keys key(t, 0) and key(t, 1)
+  const uint32_t k_at = swz(Map::col(g) * DH + E * t);
+  const uint32_t v_at0 = swz(Map::key(t, 0) * DH + VB * g), v_at1 = swz(Map::key(t, 1) * DH + VB * g);
   uint32_t stage = 0, phase = 0;           // of the ring; phase: one bit per stage
 
   while (pos < pos_end) {
-    while (a.prefix[u + 1] <= pos) ++u;
-    int64_t q0, q1;
-    user_range(a.off, u, a.B, a.total_q, &q0, &q1, a.status);
+    int64_t q0, q1, w_request;
+    int n;
+    for (;;) {
+      user_range(a.off, u, a.B, a.total_q, &q0, &q1, a.status);
+      n = kv_len(a.lens, u, most, a.status);
+      w_request = weight_of(pairs_of(q1 - q0, a.Hkv, a.G, R), n, TK);
+      if (pos < before + w_request) break;
+      before += w_request;
+      ++u;
+    }
     const int m_rows = (int)(q1 - q0);
-    const int n = kv_len(a.lens, u, (int64_t)a.max_blocks * bs, a.status);
-    const int tiles = (n + TK - 1) / TK;
     const int rts = (int)ceil_div((int64_t)m_rows * a.G, R);
-    const int64_t w_pair = tiles + kPairCost;
-    const int64_t local = pos - a.prefix[u];
-    const int64_t pair = local / w_pair;
-    const int64_t pair_pos = pos - (local - pair * w_pair);  // where the pair begins
+    const int64_t w_pair = (n + TK - 1) / TK + kPairCost;
+    const int64_t pair = div_by(pos - before, w_pair);
+    const int64_t pair_pos = before + pair * w_pair;         // where the pair begins
     const int64_t seg_end = pair_pos + w_pair < pos_end ? pair_pos + w_pair : pos_end;
-    const int h = (int)(pair / rts), rt = (int)(pair % rts);
+    const int h = (int)((uint32_t)pair / (uint32_t)rts), rt = (int)pair - h * rts;
     int t0 = (int)(pos - pair_pos) - kPairCost, t1 = (int)(seg_end - pair_pos) - kPairCost;
     if (t0 < 0) t0 = 0;
     if (t1 < 0) t1 = 0;
 
+    auto query_of = [&](int r) { return a.log_g >= 0 ? r >> a.log_g : r / a.G; };  // of row r
     // the rows' limits: row r sees keys below limit(r)
     const int r_base = rt * R, rows = m_rows * a.G - r_base < R ? m_rows * a.G - r_base : R;
     auto limit_of = [&](int r) {
       if (!a.causal) return n;
-      const int lim = n - m_rows + (r_base + r) / a.G + 1;
+      const int lim = n - m_rows + query_of(r_base + r) + 1;
       return lim < 0 ? 0 : lim;
     };
     const int lim_low = limit_of(0), lim_high = limit_of(rows - 1);
     const int t_live = (lim_high + TK - 1) / TK;
     if (t1 > t_live) t1 = t_live;
 
-    // ---- queries: fp16 fragments of rows scaled to [2^14, 2^15)
-    uint32_t qf[MT][KS][NQ][4];
-    float c_row[MT][2];
-    int lim[MT][2];
+    float o[MT][NT][4], m[MT][2], vref = 0.0f;
+    uint64_t l[MT][2];                   // sums of the even and the odd columns
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.0f;
+    }
+
+    // ---- queries, raw: asked for before the tiles, which would delay them
+    constexpr int NV = E * (int)sizeof(T) / 16 > 0 ? E * (int)sizeof(T) / 16 : 1;
+    uint4 raw[MT][2][NV];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int r = mt * 16 + hf * 8 + g;
-        float x[E];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) raw[mt][hf][i] = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-          const int rr = r_base + r;
-          const T* src = (const T*)a.Q + (q0 + rr / a.G) * a.ldq +
-                         (int64_t)(h * a.G + rr % a.G) * DH + E * t;
+          const int rr = r_base + r, qi = query_of(rr);
+          const T* src = (const T*)a.Q + (q0 + qi) * a.ldq + (h * a.G + rr - qi * a.G) * DH + E * t;
+          if constexpr (E * sizeof(T) >= 16) {
 #pragma unroll
-          for (int d = 0; d < E; d += 16 / (int)sizeof(T) > E ? E : 16 / (int)sizeof(T)) {
-            if constexpr (sizeof(T) == 4) {
-              const float4 v = *reinterpret_cast<const float4*>(src + d);
-              x[d] = v.x, x[d + 1] = v.y, x[d + 2] = v.z, x[d + 3] = v.w;
-            } else if constexpr (E >= 8) {
-              unpack8(*reinterpret_cast<const uint4*>(src + d), x + d);
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(src + d);
-              const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-              const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-              x[d] = f0.x, x[d + 1] = f0.y, x[d + 2] = f1.x, x[d + 3] = f1.y;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int d = 0; d < E; ++d) x[d] = 0.0f;
-        }
-        lim[mt][hf] = r < rows ? limit_of(r) : 0;
-        float top = 0.0f;
-#pragma unroll
-        for (int d = 0; d < E; ++d) top = fmaxf(top, fabsf(x[d]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e <= top < 2^(e+1); times 2^(14-e) in two exact factors
-        const int e = top > 0.0f ? ilogbf(fminf(top, 3.402823466e38f)) : 14;
-        const int e1 = (14 - e) / 2, e2 = 14 - e - e1;
-        const float s1 = __int_as_float((e1 + 127) << 23) * (a.negative ? -1.0f : 1.0f);
-        const float s2 = __int_as_float((e2 + 127) << 23);
-        c_row[mt][hf] = a.scale_log2 / __int_as_float((e1 + 127) << 23) / s2;
-#pragma unroll
-        for (int w = 0; w < KS; ++w) {
-          float y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = x[4 * w + i] * s1 * s2;
-          const uint32_t h0 = half2_of(y[0], y[1]), h1 = half2_of(y[2], y[3]);
-          qf[mt][w][0][hf] = h0;
-          qf[mt][w][0][hf + 2] = h1;
-          if constexpr (kSplit) {
-            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-            qf[mt][w][NQ - 1][hf] = half2_of(y[0] - f0.x, y[1] - f0.y);
-            qf[mt][w][NQ - 1][hf + 2] = half2_of(y[2] - f1.x, y[3] - f1.y);
+            for (int i = 0; i < NV; ++i) raw[mt][hf][i] = reinterpret_cast<const uint4*>(src)[i];
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            raw[mt][hf][0] = make_uint4(v.x, v.y, 0, 0);
           }
         }
       }
-    }
-
-    float o[MT][NT][4], m[MT][2], l[MT][2], vref = 0.0f;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.0f;
     }
 
     // ---- table entries and scales of 32 / nb tiles ahead, one block per lane
@@ -387,8 +484,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       ent = -1;
       sc = make_float2(-1.0f, 0.0f);     // a negative key scale hides the block
       if (j < count && lane < batch * nb) {
-        const int64_t key = (int64_t)(t0 + warp + j * kWarps) * TK;
-        const int64_t col = key / bs + lane % nb;
+        const int col = (((t0 + warp + j * kWarps) * TK) >> a.log_block) + lane % nb;
         if (col < n_cols) {
           const int b = a.table[u * a.max_blocks + col];
           if (b >= 0 && b < a.n_blocks) {
@@ -418,7 +514,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         mbar_arrive_expect_tx(&full[warp][st], (uint32_t)__popc(live) * box_bytes * 2);
       __syncwarp();
       if (ok) {
-        const int row = bs >= TK ? (int)(((int64_t)(t0 + warp + j * kWarps) * TK) % bs) * DH / 128 : 0;
+        const int row = bs >= TK ? (((t0 + warp + j * kWarps) * TK) & (bs - 1)) * DH / 128 : 0;
         uint8_t* dst = ring + st * 2 * Tile<DH>::kBytes + lane * box_bytes;
         const int z = b * a.Hkv + h;
         asm volatile(
@@ -442,6 +538,53 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
     }
 
+    // ---- queries: fp16 fragments of rows scaled to [2^14, 2^15)
+    uint32_t qf[MT][KS][NQ][4];
+    float c_row[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float x[E < 8 ? 8 : E];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if constexpr (sizeof(T) == 2) {
+            unpack8(raw[mt][hf][i], x + 8 * i);
+          } else {
+            x[4 * i] = __uint_as_float(raw[mt][hf][i].x), x[4 * i + 1] = __uint_as_float(raw[mt][hf][i].y);
+            x[4 * i + 2] = __uint_as_float(raw[mt][hf][i].z), x[4 * i + 3] = __uint_as_float(raw[mt][hf][i].w);
+          }
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int d = 0; d < E; ++d) top = fmaxf(top, fabsf(x[d]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e <= top < 2^(e+1): times 2^(14-e), as two exact factors
+        const int exp = (__float_as_int(top) >> 23) & 255;
+        const int shift = 14 + 127 - (exp < 254 ? exp : 254);
+        const int e1 = shift >> 1, e2 = shift - e1;
+        const float s1 = __int_as_float((127 + e1) << 23) * (a.negative ? -1.0f : 1.0f);
+        const float s2 = __int_as_float((127 + e2) << 23);
+        c_row[mt][hf] = a.scale_log2 * __int_as_float((127 - e1) << 23) * __int_as_float((127 - e2) << 23);
+#pragma unroll
+        for (int w = 0; w < KS; ++w) {
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = x[4 * w + i] * s1 * s2;
+          const uint32_t h0 = half2_of(y[0], y[1]), h1 = half2_of(y[2], y[3]);
+          qf[mt][w][0][hf] = h0;
+          qf[mt][w][0][hf + 2] = h1;
+          if constexpr (kSplit) {
+            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            qf[mt][w][NQ - 1][hf] = half2_of(y[0] - f0.x, y[1] - f0.y);
+            qf[mt][w][NQ - 1][hf + 2] = half2_of(y[2] - f1.x, y[3] - f1.y);
+          }
+        }
+      }
+    }
+
     for (int j = 0; j < count; ++j) {
       if (j - base == batch) {           // batch 0 is used up
         base += batch;
@@ -449,171 +592,187 @@ __global__ void __launch_bounds__(kWarps * 32)
         sc0 = sc1;
         load_batch(base + batch, ent1, sc1);
       }
-      const uint32_t ks = ring_u32 + stage * 2 * Tile<DH>::kBytes, vs = ks + Tile<DH>::kBytes;
+      const uint8_t *ks = ring + stage * 2 * Tile<DH>::kBytes, *vs = ks + Tile<DH>::kBytes;
       mbar_wait(&full[warp][stage], (phase >> stage) & 1u, a.status, &abort_flag);
       phase ^= 1u << stage;
 
-      // ---- scores
-      float s[MT][2 * NG][4];
-#pragma unroll
-      for (int x = 0; x < 2 * NG; ++x) {
-        const int key = (x >> 1) * 16 + kcol + (x & 1) * Map::odd;
-        uint32_t w[KS];
-        if constexpr (E >= 16) {
-#pragma unroll
-          for (int c = 0; c < E; c += 16) lds<16>(ks + swz(key * DH + E * t + c), w + c / 4);
-        } else {
-          lds<E>(ks + swz(key * DH + E * t), w);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][x][i] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint32_t b = w[k] ^ 0x80808080u;
-          const uint32_t b0 = codes_to_half2<0x4140>(b), b1 = codes_to_half2<0x4342>(b);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int p = 0; p < NQ; ++p) mma16816(s[mt][x], qf[mt][k][p], b0, b1);
-        }
-      }
+#pragma unroll 1
+      for (int sub = 0; sub < TK; sub += SK) {
+        const int key0 = (t0 + warp + j * kWarps) * TK + sub;
+        if (key0 >= lim_high) break;
+        const uint32_t flip = ((sub * DH >> 7) & 7) << 4;  // of the step's first row (0 but for DH 16)
 
-      // ---- the groups' scales; hidden keys
-      float kg[NG], vg[NG];
-      bool hidden = false;
-      float vmax = 0.0f;
-#pragma unroll
-      for (int x = 0; x < NG; ++x) {
-        const int src = (j - base) * nb + (nb > 1 ? x * 16 / bs : 0);
-        kg[x] = __shfl_sync(0xffffffffu, sc0.x, src);
-        vg[x] = __shfl_sync(0xffffffffu, sc0.y, src);
-        hidden |= kg[x] < 0.0f;
-        vmax = fmaxf(vmax, vg[x]);
-      }
-      const int key0 = (t0 + warp + j * kWarps) * TK;
-      if (hidden || key0 + TK > lim_low) {
+        // ---- scores
+        float s[MT][2 * NG][4];
 #pragma unroll
         for (int x = 0; x < 2 * NG; ++x) {
-          const int key = key0 + (x >> 1) * 16 + (x & 1) * Map::odd;
-          const bool off = kg[x >> 1] < 0.0f;
-          const int ka = key + Map::col(2 * t), kb = key + Map::col(2 * t + 1);
+          const uint32_t row = ((x >> 1) * 16 + (x & 1) * Map::odd) * DH;
+          uint32_t w[KS];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if (off || ka >= lim[mt][0]) s[mt][x][0] = -INFINITY;
-            if (off || kb >= lim[mt][0]) s[mt][x][1] = -INFINITY;
-            if (off || ka >= lim[mt][1]) s[mt][x][2] = -INFINITY;
-            if (off || kb >= lim[mt][1]) s[mt][x][3] = -INFINITY;
-          }
-        }
-        // the marker is no factor
+          for (int c = 0; c < E; c += 16)
+            lds<E < 16 ? E : 16>(ks + sub * DH + (swz_at(k_at, row) ^ c ^ flip), w + c / 4);
 #pragma unroll
-        for (int x = 0; x < NG; ++x)
-          if (kg[x] < 0.0f) kg[x] = 1.0f;
-      }
-
-      // ---- running maximum (in units of log2) and value unit
-      float top[MT][2];
-      bool grow = vmax > vref;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float best = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < NG; ++x) {
-            const float v = fmaxf(fmaxf(s[mt][2 * x][2 * hf], s[mt][2 * x][2 * hf + 1]),
-                                  fmaxf(s[mt][2 * x + 1][2 * hf], s[mt][2 * x + 1][2 * hf + 1]));
-            best = fmaxf(best, v * fmaxf(c_row[mt][hf] * kg[x], kTiny));
-          }
-          top[mt][hf] = best;
-          grow |= best > m[mt][hf];
-        }
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-        const float vnew = fmaxf(vref, vmax);
-        const float vkeep = vnew > 0.0f ? vref / vnew : 0.0f;
-        vref = vnew;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float v = top[mt][hf];
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            v = fmaxf(v, m[mt][hf]);
-            const float keep = ex2(m[mt][hf] - (v == -INFINITY ? 0.0f : v));
-            m[mt][hf] = v;
-            l[mt][hf] *= keep;
-            const float ok = keep * vkeep;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              o[mt][i][2 * hf] *= ok;
-              o[mt][i][2 * hf + 1] *= ok;
-            }
-          }
-        }
-      }
-
-      // ---- probabilities times their block's value scale over the unit
-      uint32_t pf[MT][NG][NQ][4];
-#pragma unroll
-      for (int x = 0; x < NG; ++x) {
-        // log2 of the ratio, at least 2^-60 (what is smaller adds nothing)
-        const float lr = vref > 0.0f ? fmaxf(__log2f(vg[x] / vref), -60.0f) : 0.0f;
-        const float inv = ex2(-lr);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float c = fmaxf(c_row[mt][hf] * kg[x], kTiny);
-            const float add = kOffset + lr - (m[mt][hf] == -INFINITY ? 0.0f : m[mt][hf]);
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float v = s[mt][2 * x + (i >> 1)][2 * hf + (i & 1)];
-              p[i] = ex2(fmaf(v, c, add));
-            }
-            l[mt][hf] = fmaf((p[0] + p[1]) + (p[2] + p[3]), inv, l[mt][hf]);
-            const uint32_t h0 = half2_sat(p[0], p[1]), h1 = half2_sat(p[2], p[3]);
-            pf[mt][x][0][hf] = h0;
-            pf[mt][x][0][hf + 2] = h1;
-            if constexpr (kSplit) {
-              const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-              const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-              pf[mt][x][NQ - 1][hf] = half2_of(p[0] - f0.x, p[1] - f0.y);
-              pf[mt][x][NQ - 1][hf + 2] = half2_of(p[2] - f1.x, p[3] - f1.y);
-            }
-          }
-        }
-      }
-
-      // ---- values
-#pragma unroll
-      for (int x = 0; x < NG; ++x) {
-        constexpr int W = VB < 4 ? 1 : VB / 4;
-        uint32_t w[4][W];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lds<VB>(vs + swz((x * 16 + Map::key(t, i)) * DH + VB * g), w[i]);
-#pragma unroll
-          for (int c = 0; c < W; ++c) w[i][c] ^= 0x80808080u;
-        }
-#pragma unroll
-        for (int c = 0; c < W; ++c) {
-          // bytes of two keys side by side, two dims at a time
-          const uint32_t ab0 = __byte_perm(w[0][c], w[1][c], 0x5140), cd0 = __byte_perm(w[2][c], w[3][c], 0x5140);
-          const uint32_t ab1 = __byte_perm(w[0][c], w[1][c], 0x7362), cd1 = __byte_perm(w[2][c], w[3][c], 0x7362);
-#pragma unroll
-          for (int i = 0; i < (VB < 4 ? VB : 4); ++i) {
-            const uint32_t ab = i < 2 ? ab0 : ab1, cd = i < 2 ? cd0 : cd1;
-            const uint32_t b0 = (i & 1) ? codes_to_half2<0x4342>(ab) : codes_to_half2<0x4140>(ab);
-            const uint32_t b1 = (i & 1) ? codes_to_half2<0x4342>(cd) : codes_to_half2<0x4140>(cd);
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t b = w[k] ^ 0x80808080u;
+            const uint32_t b0 = codes_to_half2<0x4140>(b), b1 = codes_to_half2<0x4342>(b);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int p = 0; p < NQ; ++p) mma16816(o[mt][4 * c + i], pf[mt][x][p], b0, b1);
+              for (int p = 0; p < NQ; ++p) {
+                if (k + p == 0) mma16816_first(s[mt][x], qf[mt][k][p], b0, b1);
+                else mma16816(s[mt][x], qf[mt][k][p], b0, b1);
+              }
+          }
+        }
+
+        // ---- the blocks' scales; hidden keys
+        float kg[NC], vg[NC];
+        bool hidden = false;
+        float vmax = 0.0f;
+#pragma unroll
+        for (int x = 0; x < NC; ++x) {
+          const int src = (j - base) * nb + (nb > 1 ? (sub + x * 16) >> a.log_block : 0);
+          kg[x] = __shfl_sync(0xffffffffu, sc0.x, src);
+          vg[x] = __shfl_sync(0xffffffffu, sc0.y, src);
+          hidden |= kg[x] < 0.0f;
+          vmax = fmaxf(vmax, vg[x]);
+        }
+        if (hidden || key0 + SK > lim_low) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int r = mt * 16 + hf * 8 + g;
+              const int lim = r < rows ? limit_of(r) : 0;
+#pragma unroll
+              for (int x = 0; x < 2 * NG; ++x) {
+                const int key = key0 + (x >> 1) * 16 + (x & 1) * Map::odd;
+                const bool off = kg[ONE ? 0 : x >> 1] < 0.0f;
+                if (off || key + Map::col(2 * t) >= lim) s[mt][x][2 * hf] = -INFINITY;
+                if (off || key + Map::col(2 * t + 1) >= lim) s[mt][x][2 * hf + 1] = -INFINITY;
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < NC; ++x)
+            if (kg[x] < 0.0f) kg[x] = 1.0f;  // the marker is no factor
+        }
+
+        // ---- running maximum (in units of log2) and value unit
+        float top[MT][2];
+        bool grow = vmax > vref;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float best = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < NG; ++x) {
+              const float v = fmaxf(fmaxf(s[mt][2 * x][2 * hf], s[mt][2 * x][2 * hf + 1]),
+                                    fmaxf(s[mt][2 * x + 1][2 * hf], s[mt][2 * x + 1][2 * hf + 1]));
+              best = ONE ? fmaxf(best, v) : fmaxf(best, v * fmaxf(c_row[mt][hf] * kg[ONE ? 0 : x], kTiny));
+            }
+            if (ONE) best *= fmaxf(c_row[mt][hf] * kg[0], kTiny);
+            top[mt][hf] = best;
+            grow |= best > m[mt][hf] + kSlack;
+          }
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          const float vnew = fmaxf(vref, vmax);
+          const float vkeep = vnew > 0.0f ? vref / vnew : 0.0f;
+          vref = vnew;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float v = top[mt][hf];
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+              v = fmaxf(v, m[mt][hf]);
+              const float keep = ex2(m[mt][hf] - (v == -INFINITY ? 0.0f : v));
+              m[mt][hf] = v;
+              l[mt][hf] = mul2(l[mt][hf], pack2(keep, keep));
+              const uint64_t ok = pack2(keep * vkeep, keep * vkeep);
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                unpack2(mul2(pack2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]), ok), o[mt][i][2 * hf],
+                       o[mt][i][2 * hf + 1]);
+            }
+          }
+        }
+
+        // ---- probabilities times their block's value scale over the unit:
+        // log2 of the ratio joins the exponent, at least -60 (what is smaller
+        // adds nothing); the sum takes it out again
+        float lr[NC], inv[NC];
+#pragma unroll
+        for (int x = 0; x < NC; ++x) {
+          const float ratio = __log2f(__fdividef(vg[x], vref));
+          lr[x] = vref > 0.0f ? (ratio > -60.0f ? ratio : -60.0f) : 0.0f;
+          inv[x] = ex2(-lr[x]);
+        }
+        uint32_t pf[MT][NG][NQ][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float from = kOffset - (m[mt][hf] == -INFINITY ? 0.0f : m[mt][hf]);
+#pragma unroll
+            for (int x = 0; x < NG; ++x) {
+              const float c = fmaxf(c_row[mt][hf] * kg[ONE ? 0 : x], kTiny);
+              const float add = from + lr[ONE ? 0 : x];
+              float p[4];
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                unpack2(fma2(pack2(s[mt][2 * x + (i >> 1)][2 * hf], s[mt][2 * x + (i >> 1)][2 * hf + 1]),
+                            pack2(c, c), pack2(add, add)),
+                       p[i], p[i + 1]);
+                p[i] = ex2(p[i]);
+                p[i + 1] = ex2(p[i + 1]);
+              }
+              const float by = inv[ONE ? 0 : x];
+              l[mt][hf] = fma2(add2(pack2(p[0], p[1]), pack2(p[2], p[3])), pack2(by, by), l[mt][hf]);
+              const uint32_t h0 = half2_sat(p[0], p[1]), h1 = half2_sat(p[2], p[3]);
+              pf[mt][x][0][hf] = h0;
+              pf[mt][x][0][hf + 2] = h1;
+              if constexpr (kSplit) {
+                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                pf[mt][x][NQ - 1][hf] = half2_of(p[0] - f0.x, p[1] - f0.y);
+                pf[mt][x][NQ - 1][hf + 2] = half2_of(p[2] - f1.x, p[3] - f1.y);
+              }
+            }
+          }
+        }
+
+        // ---- values
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+          constexpr int W = VB < 4 ? 1 : VB / 4;
+          uint32_t w[4][W];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lds<VB>(vs + sub * DH +
+                        (swz_at(i & 1 ? v_at1 : v_at0, (x * 16 + (i >> 1) * Map::odd) * DH) ^ flip),
+                    w[i]);
+#pragma unroll
+            for (int c = 0; c < W; ++c) w[i][c] ^= 0x80808080u;
+          }
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            // bytes of two keys side by side, two dims at a time
+            const uint32_t ab0 = __byte_perm(w[0][c], w[1][c], 0x5140), cd0 = __byte_perm(w[2][c], w[3][c], 0x5140);
+            const uint32_t ab1 = __byte_perm(w[0][c], w[1][c], 0x7362), cd1 = __byte_perm(w[2][c], w[3][c], 0x7362);
+#pragma unroll
+            for (int i = 0; i < (VB < 4 ? VB : 4); ++i) {
+              const uint32_t ab = i < 2 ? ab0 : ab1, cd = i < 2 ? cd0 : cd1;
+              const uint32_t b0 = (i & 1) ? codes_to_half2<0x4342>(ab) : codes_to_half2<0x4140>(ab);
+              const uint32_t b1 = (i & 1) ? codes_to_half2<0x4342>(cd) : codes_to_half2<0x4140>(cd);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int p = 0; p < NQ; ++p) mma16816(o[mt][4 * c + i], pf[mt][x][p], b0, b1);
+            }
           }
         }
       }
@@ -629,13 +788,15 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float sum = l[mt][hf];
+        float sum, odd;
+        unpack2(l[mt][hf], sum, odd);
+        sum += odd;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int r = mt * 16 + hf * 8 + g;
         if (t == 0) ml[warp][r] = make_float2(m[mt][hf], sum);
         // NaN sums stay NaN; a row that saw no key gives 0
-        const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
         float out[E];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -651,12 +812,12 @@ __global__ void __launch_bounds__(kWarps * 32)
     __syncthreads();
 
     const int64_t pair_last = pair_pos + w_pair - 1;
-    const int first_cta = (int)(pair_pos / share), last_cta = (int)(pair_last / share);
+    const int first_cta = (int)div_by(pair_pos, share), last_cta = (int)div_by(pair_last, share);
     const bool whole = first_cta == last_cta;
     float* part = a.part + (int64_t)(2 * blockIdx.x + (blockIdx.x == first_cta ? 1 : 0)) * (R * DH + 2 * R);
     auto store = [&](int r, int d, float4 v, float top, float sum) {
-      const int rr = r_base + r;
-      const int64_t at = (q0 + rr / a.G) * a.Hq + h * a.G + rr % a.G;
+      const int rr = r_base + r, qi = query_of(rr);
+      const int64_t at = (q0 + qi) * a.Hq + h * a.G + rr - qi * a.G;
       T* dst = (T*)a.O + at * DH + d;
       if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4*>(dst) = v;
@@ -680,7 +841,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         x[w].y *= ex2(x[w].x - (top == -INFINITY ? 0.0f : top));
         sum += x[w].y;
       }
-      const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -702,24 +863,42 @@ __global__ void __launch_bounds__(kWarps * 32)
       if (threadIdx.x == 0) is_last = atomicAdd(a.tickets + first_cta, 1) == last_cta - first_cta;
       __syncthreads();
       if (is_last) {
+        if (threadIdx.x == 0) a.tickets[first_cta] = 0;
         __threadfence();
         const int64_t pitch = R * DH + 2 * R;
         auto slot = [&](int c) { return a.part + (2 * (int64_t)c + (c == first_cta ? 1 : 0)) * pitch; };
         for (int i = threadIdx.x; i < rows * (DH / 4); i += kWarps * 32) {
           const int r = i / (DH / 4), d = i % (DH / 4) * 4;
-          float top = -INFINITY;
-          for (int c = first_cta; c <= last_cta; ++c)
-            top = fmaxf(top, __ldcg(slot(c) + R * DH + 2 * r));
-          float sum = 0.0f;
+          float top = -INFINITY, sum = 0.0f;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c = first_cta; c <= last_cta; ++c) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(slot(c) + R * DH + 2 * r));
-            const float k = x.y * ex2(x.x - (top == -INFINITY ? 0.0f : top));
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(slot(c) + r * DH + d));
-            sum += k;
-            v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+          for (int c0 = first_cta; c0 <= last_cta; c0 += kJoin) {
+            float2 x[kJoin];             // kJoin parts in flight
+            float4 y[kJoin];
+#pragma unroll
+            for (int c = 0; c < kJoin; ++c) {
+              x[c] = make_float2(-INFINITY, 0.0f);
+              y[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (c0 + c <= last_cta) {
+                x[c] = __ldcg(reinterpret_cast<const float2*>(slot(c0 + c) + R * DH + 2 * r));
+                y[c] = __ldcg(reinterpret_cast<const float4*>(slot(c0 + c) + r * DH + d));
+              }
+            }
+            float best = top;
+#pragma unroll
+            for (int c = 0; c < kJoin; ++c) best = fmaxf(best, x[c].x);
+            const float ref = best == -INFINITY ? 0.0f : best, keep = ex2(top - ref);
+            sum *= keep;
+            v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+            top = best;
+#pragma unroll
+            for (int c = 0; c < kJoin; ++c) {
+              const float k = x[c].y * ex2(x[c].x - ref);
+              sum += k;
+              v.x = fmaf(k, y[c].x, v.x), v.y = fmaf(k, y[c].y, v.y);
+              v.z = fmaf(k, y[c].z, v.z), v.w = fmaf(k, y[c].w, v.w);
+            }
           }
-          const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
           store(r, d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by), top, sum);
         }
       }
@@ -739,10 +918,9 @@ int pair_rows(const lime_kv_dims& D, int64_t rows_per_head) {
   return D.dtype == LIME_BF16 && D.dh <= 64 && rows_per_head > 16 ? 32 : 16;
 }
 
-template <typename T, int DH, int MT>
-int launch(const lime_kv_dims& D, Args a, CUtensorMap mk, CUtensorMap mv, Plan* plan,
-           int64_t* prefix, cudaStream_t st) {
-  auto kernel = k_kv_attn<T, DH, MT>;
+template <typename T, int DH, int MT, bool ONE>
+int launch(Args a, CUtensorMap mk, CUtensorMap mv, int64_t* prefix, cudaStream_t st) {
+  auto kernel = k_kv_attn<T, DH, MT, ONE>;
   const size_t smem = kWarps * Tile<DH>::kRing + 1024;
   static int per_sm[64] = {0};
   int dev = 0;
@@ -759,34 +937,35 @@ int launch(const lime_kv_dims& D, Args a, CUtensorMap mk, CUtensorMap mv, Plan* 
   }
   int grid = num_sms() * per_sm[dev];
   if (grid > kMaxCtas) grid = kMaxCtas;
-  int rc = launch_pdl(k_kv_plan, dim3(1), dim3(1024), 0, st, 1, a.B, a.off, a.total_q, a.lens,
-                      a.Hkv, a.G, (int64_t)a.max_blocks * a.block, 16 * MT, (int)Tile<DH>::TK, grid,
-                      plan, prefix, a.tickets, a.status);
-  if (rc) return rc;
+  if (a.B > kInlineRequests) {
+    a.prefix = prefix;
+    const int rc = launch_pdl(k_kv_plan, dim3(1), dim3(1024), 0, st, 1, a.B, a.off, a.total_q, a.lens,
+                              a.Hkv, a.G, (int64_t)a.max_blocks << a.log_block, 16 * MT,
+                              (int)Tile<DH>::TK, prefix, a.status);
+    if (rc) return rc;
+  }
   return launch_pdl(kernel, dim3(grid), dim3(kWarps * 32), smem, st, 1, mk, mv, a);
 }
 
 }  // namespace
 
-size_t kv_ws_bytes(const lime_kv_dims& D, int64_t B, int64_t total_q) {
-  const size_t ranks = (size_t)B * 8;  // of the requests' blocks (reserve, release)
-  if (total_q == 0) return ranks;
-  const size_t attn = 256 + ((size_t)(B + 1) * 8 + 255) / 256 * 256 + kMaxCtas * 4 +
-                      2 * kMaxCtas * part_floats(D.dh <= 64 ? 32 : 16, D.dh) * 4;
-  return attn > ranks ? attn : ranks;
+size_t kv_ticket_bytes() { return kMaxCtas * sizeof(int); }
+
+size_t kv_attention_ws_bytes(const lime_kv_dims& D, int64_t B, int64_t total_q) {
+  if (total_q == 0) return 0;
+  const size_t prefix = B > kInlineRequests ? ((size_t)(B + 2) * 8 + 255) / 256 * 256 : 0;
+  return prefix + 2 * kMaxCtas * part_floats(D.dh <= 64 ? 32 : 16, D.dh) * 4;
 }
 
 int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, const int64_t* off,
                  int64_t total_q, const int32_t* table, const int32_t* lens, const int8_t* kc,
                  const int8_t* vc, const float* scale, float sm_scale, bool causal, void* O,
-                 float* lse, void* ws, unsigned* status, cudaStream_t st) {
+                 float* lse, void* ws, int* tickets, unsigned* status, cudaStream_t st) {
   const int G = D.Hq / D.Hkv;
   const int R = pair_rows(D, ceil_div(total_q, B) * G);
   const int TK = D.dh == 128 ? 32 : 64;
-  char* p = (char*)ws;
-  Plan* plan = (Plan*)p;
-  int64_t* prefix = (int64_t*)(p + 256);
-  p += 256 + ((size_t)(B + 1) * 8 + 255) / 256 * 256;
+  int64_t* prefix = (int64_t*)ws;
+  const size_t prefix_bytes = B > kInlineRequests ? ((size_t)(B + 2) * 8 + 255) / 256 * 256 : 0;
 
   CUtensorMap mk, mv;
   const int box = D.block < TK ? D.block : TK;
@@ -796,12 +975,19 @@ int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, c
   Args a = {};
   a.Q = Q, a.ldq = ldq, a.off = off, a.table = table, a.lens = lens;
   a.scale = (const float2*)scale;
-  a.plan = plan, a.prefix = prefix, a.tickets = (int*)p, a.part = (float*)(p + kMaxCtas * 4);
+  a.tickets = tickets, a.part = (float*)((char*)ws + prefix_bytes);
   a.O = O, a.lse = lse, a.status = status;
   a.B = B, a.total_q = total_q, a.n_blocks = D.n_blocks;
-  a.Hq = D.Hq, a.Hkv = D.Hkv, a.G = G, a.block = D.block, a.max_blocks = D.max_blocks;
+  a.Hq = D.Hq, a.Hkv = D.Hkv, a.G = G, a.max_blocks = D.max_blocks;
+  a.log_block = 4;
+  while (1 << a.log_block < D.block) ++a.log_block;
+  a.log_g = (G & (G - 1)) ? -1 : 0;
+  while (a.log_g >= 0 && 1 << a.log_g < G) ++a.log_g;
   a.scale_log2 = fabsf(sm_scale) * kLog2e, a.negative = sm_scale < 0.0f, a.causal = causal;
-#define RUN(T, DH, MT) return launch<T, DH, MT>(D, a, mk, mv, plan, prefix, st)
+#define RUN(T, DH, MT)                                                 \
+  return D.block >= Tile<DH>::SK                                       \
+             ? launch<T, DH, MT, true>(a, mk, mv, prefix, st) \
+             : launch<T, DH, MT, false>(a, mk, mv, prefix, st)
   if (D.dtype == LIME_BF16) {
     if (D.dh == 16) { if (R == 32) RUN(bf16, 16, 2); RUN(bf16, 16, 1); }
     if (D.dh == 32) { if (R == 32) RUN(bf16, 32, 2); RUN(bf16, 32, 1); }

@@ -19,7 +19,10 @@ __device__ __forceinline__ int kv_len(const int32_t* lens, int64_t u, int64_t mo
   return n;
 }
 
-size_t kv_ws_bytes(const lime_kv_dims& D, int64_t B, int64_t total_q);
+// Scratch of an attention call, apart from its tickets: counters that are zero
+// between calls and stand at a fixed place of the workspace.
+size_t kv_attention_ws_bytes(const lime_kv_dims& D, int64_t B, int64_t total_q);
+size_t kv_ticket_bytes();
 
 int kv_reserve(const lime_kv_dims& D, int64_t B, const int32_t* lens, const int64_t* off,
                int64_t total, int32_t* table, const int32_t* free_blocks, int64_t free_cap,
@@ -35,6 +38,6 @@ int kv_append(const lime_kv_dims& D, const void* K, int64_t ldk, const void* V, 
 int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, const int64_t* off,
                  int64_t total_q, const int32_t* table, const int32_t* lens, const int8_t* kc,
                  const int8_t* vc, const float* scale, float sm_scale, bool causal, void* O,
-                 float* lse, void* ws, unsigned* status, cudaStream_t st);
+                 float* lse, void* ws, int* tickets, unsigned* status, cudaStream_t st);
 
 }  // namespace lime

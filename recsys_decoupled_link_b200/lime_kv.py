@@ -14,8 +14,7 @@ from typing import Optional
 
 import torch
 
-from .lime import (LIME_BF16, LIME_ERR_SHAPE, LIME_F32, LimeError, _lib, lime_get_status,
-                   lime_workspace_init)
+from .lime import LIME_BF16, LIME_ERR_SHAPE, LIME_F32, LimeError, _lib, lime_get_status
 
 LIME_FLAG_BAD_BLOCK, LIME_FLAG_NO_BLOCKS, LIME_FLAG_NONFINITE = 8, 16, 32
 
@@ -31,6 +30,7 @@ def _sign():
     D = ctypes.POINTER(lime_kv_dims)
     sig = {
         "lime_kv_workspace_bytes": (SZ, [D, I64, I64]),
+        "lime_kv_workspace_init": (I32, [P, SZ, P]),
         "lime_kv_reserve": (I32, [D, I64, P, P, I64, P, P, I64, P, P, P, P, P, SZ, P]),
         "lime_kv_release": (I32, [D, I64, P, P, P, P, I64, P, P, P, P, SZ, P]),
         "lime_kv_append": (I32, [D, P, I64, P, I64, I64, P, P, P, P, P, SZ, P]),
@@ -43,8 +43,8 @@ def _sign():
 
 
 _sign()
-EXPORTED = ("lime_kv_workspace_bytes", "lime_kv_reserve", "lime_kv_release", "lime_kv_append",
-            "lime_kv_attention")
+EXPORTED = ("lime_kv_workspace_bytes", "lime_kv_workspace_init", "lime_kv_reserve",
+            "lime_kv_release", "lime_kv_append", "lime_kv_attention")
 
 
 def make_kv_dims(Hq: int, Hkv: int, dh: int, block: int, n_blocks: int, max_blocks: int,
@@ -67,7 +67,7 @@ class KvWorkspace:
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
         self.nbytes, self.address = n, self.buf.data_ptr()
         self.device = self.buf.get_device()
-        lime_workspace_init(self, stream=stream)
+        lime_kv_workspace_init(self, stream=stream)
 
     @property
     def ptr(self):
@@ -125,6 +125,12 @@ def _check_pool(dims, dev, k_cache, v_cache, scale):
             and k_cache.is_contiguous() and v_cache.is_contiguous() and scale.is_contiguous()):
         _refuse(dev, None, ("k_cache", k_cache, _i8, shape), ("v_cache", v_cache, _i8, shape),
                 ("scale", scale, _f32, (shape[0], shape[1], 2)))
+
+
+def lime_kv_workspace_init(ws: KvWorkspace, stream=None):
+    rc = _lib.lime_kv_workspace_init(ws.address, ws.nbytes, _raw_stream(stream, _device()))
+    if rc:
+        raise LimeError("lime_kv_workspace_init", rc)
 
 
 def lime_kv_reserve(dims, lens, new_offsets, block_table, free_blocks, n_free, lens_out,
