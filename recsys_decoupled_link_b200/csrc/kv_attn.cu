@@ -295,6 +295,19 @@ constexpr int min_blocks() {
   return DH <= 32 ? (MT == 2 ? 2 : 4) : DH == 64 ? (MT == 2 ? 2 : 3) : (sizeof(T) == 2 ? 3 : 2);
 }
 
+// What a segment's start and end know and its tile loop hardly needs: kept in
+// shared memory, a copy per warp, for the registers it would hold meanwhile.
+struct Segment {
+  int64_t pos, pos_end;       // this block's place in the weights, and its end
+  int64_t share;              // of every block
+  int64_t u, before;          // request, and the weight before it
+  int64_t pair_pos, seg_end;  // where the pair begins and the segment ends
+  int64_t q0;                 // the request's first query row
+  int n, m_rows;              // its cached and its query rows
+  int r_base, rows;           // the pair's rows (query, head of the group)
+  int w_pair;
+};
+
 // ONE: a softmax step's keys lie in one block (block >= SK), under one scale.
 template <typename T, int DH, int MT, bool ONE>
 __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
@@ -315,6 +328,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   __shared__ uint64_t full[kWarps][S];
   __shared__ float2 ml[kWarps][R];
   __shared__ int abort_flag, is_last;
+  __shared__ Segment segments[kWarps];
   __shared__ int64_t warp_sum[kWarps], warp_pairs[kWarps], found[2];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1,024-byte aligned: the swizzle's period
 
@@ -393,8 +407,16 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     u = found[0];
     before = found[1];
   }
-  int64_t pos = share * blockIdx.x;
-  const int64_t pos_end = pos + share < total ? pos + share : total;
+  volatile Segment& sg = segments[warp];
+  if (lane == 0) {
+    const int64_t pos = share * blockIdx.x;
+    sg.pos = pos;
+    sg.pos_end = pos + share < total ? pos + share : total;
+    sg.share = share;
+    sg.u = u;
+    sg.before = before;
+  }
+  __syncwarp();
 
   const int nb = bs >= TK ? 1 : TK / bs;   // blocks of a tile
   const int box_rows = bs >= TK ? TK : bs;
@@ -406,8 +428,9 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   const uint32_t v_at0 = swz(Map::key(t, 0) * DH + VB * g), v_at1 = swz(Map::key(t, 1) * DH + VB * g);
   uint32_t stage = 0, phase = 0;           // of the ring; phase: one bit per stage
 
-  while (pos < pos_end) {
-    int64_t q0, q1, w_request;
+  while (sg.pos < sg.pos_end) {
+    const int64_t pos = sg.pos, pos_end = sg.pos_end;
+    int64_t u = sg.u, before = sg.before, q0, q1, w_request;
     int n;
     for (;;) {
       user_range(a.off, u, a.B, a.total_q, &q0, &q1, a.status);
@@ -431,9 +454,17 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     auto query_of = [&](int r) { return a.log_g >= 0 ? r >> a.log_g : r / a.G; };  // of row r
     // the rows' limits: row r sees keys below limit(r)
     const int r_base = rt * R, rows = m_rows * a.G - r_base < R ? m_rows * a.G - r_base : R;
+    __syncwarp();
+    if (lane == 0) {
+      sg.u = u, sg.before = before;
+      sg.pair_pos = pair_pos, sg.seg_end = seg_end, sg.q0 = q0;
+      sg.n = n, sg.m_rows = m_rows, sg.r_base = r_base, sg.rows = rows;
+      sg.w_pair = (int)w_pair;
+    }
+    __syncwarp();
     auto limit_of = [&](int r) {
-      if (!a.causal) return n;
-      const int lim = n - m_rows + query_of(r_base + r) + 1;
+      if (!a.causal) return (int)sg.n;
+      const int lim = sg.n - sg.m_rows + query_of(sg.r_base + r) + 1;
       return lim < 0 ? 0 : lim;
     };
     const int lim_low = limit_of(0), lim_high = limit_of(rows - 1);
@@ -478,15 +509,14 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
 
     // ---- table entries and scales of 32 / nb tiles ahead, one block per lane
     const int count = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
-    const int n_cols = (n + bs - 1) / bs;
     auto load_batch = [&](int first, int& ent, float2& sc) {
       const int j = first + lane / nb;
       ent = -1;
       sc = make_float2(-1.0f, 0.0f);     // a negative key scale hides the block
       if (j < count && lane < batch * nb) {
         const int col = (((t0 + warp + j * kWarps) * TK) >> a.log_block) + lane % nb;
-        if (col < n_cols) {
-          const int b = a.table[u * a.max_blocks + col];
+        if (col < (sg.n + bs - 1) >> a.log_block) {
+          const int b = a.table[sg.u * a.max_blocks + col];
           if (b >= 0 && b < a.n_blocks) {
             ent = b;
             sc = a.scale[(int64_t)b * a.Hkv + h];
@@ -643,7 +673,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const int r = mt * 16 + hf * 8 + g;
-              const int lim = r < rows ? limit_of(r) : 0;
+              const int lim = r < sg.rows ? limit_of(r) : 0;
 #pragma unroll
               for (int x = 0; x < 2 * NG; ++x) {
                 const int key = key0 + (x >> 1) * 16 + (x & 1) * Map::odd;
@@ -811,13 +841,15 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     }
     __syncthreads();
 
-    const int64_t pair_last = pair_pos + w_pair - 1;
-    const int first_cta = (int)div_by(pair_pos, share), last_cta = (int)div_by(pair_last, share);
+    const int first_cta = (int)div_by(sg.pair_pos, sg.share);
+    const int last_cta = (int)div_by(sg.pair_pos + sg.w_pair - 1, sg.share);
+    const int out_rows = sg.rows;
+    const int64_t q_first = sg.q0;
     const bool whole = first_cta == last_cta;
     float* part = a.part + (int64_t)(2 * blockIdx.x + (blockIdx.x == first_cta ? 1 : 0)) * (R * DH + 2 * R);
     auto store = [&](int r, int d, float4 v, float top, float sum) {
-      const int rr = r_base + r, qi = query_of(rr);
-      const int64_t at = (q0 + qi) * a.Hq + h * a.G + rr - qi * a.G;
+      const int rr = sg.r_base + r, qi = query_of(rr);
+      const int64_t at = (q_first + qi) * a.Hq + h * a.G + rr - qi * a.G;
       T* dst = (T*)a.O + at * DH + d;
       if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4*>(dst) = v;
@@ -826,7 +858,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       }
       if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - kOffset) * kLn2;
     };
-    for (int i = threadIdx.x; i < rows * (DH / 4); i += kWarps * 32) {
+    for (int i = threadIdx.x; i < out_rows * (DH / 4); i += kWarps * 32) {
       const int r = i / (DH / 4), d = i % (DH / 4) * 4;
       float2 x[kWarps];
       float top = -INFINITY;
@@ -867,7 +899,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         __threadfence();
         const int64_t pitch = R * DH + 2 * R;
         auto slot = [&](int c) { return a.part + (2 * (int64_t)c + (c == first_cta ? 1 : 0)) * pitch; };
-        for (int i = threadIdx.x; i < rows * (DH / 4); i += kWarps * 32) {
+        for (int i = threadIdx.x; i < out_rows * (DH / 4); i += kWarps * 32) {
           const int r = i / (DH / 4), d = i % (DH / 4) * 4;
           float top = -INFINITY, sum = 0.0f;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -905,7 +937,8 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     }
     fence_proxy_async_smem();            // the ring's next writes are TMA's
     __syncthreads();
-    pos = seg_end;
+    if (lane == 0) sg.pos = sg.seg_end;
+    __syncwarp();
   }
 }
 
