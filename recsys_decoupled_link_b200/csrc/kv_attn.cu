@@ -31,9 +31,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxCtas = 640;       // most blocks of the persistent grid
-constexpr int kPairCost = 12;       // a pair's fixed cost, in tiles
+constexpr int kMaxWorkers = kWarps * kMaxCtas;
+// A pair's fixed cost, in tiles of a worker of NW warps.
+__host__ __device__ constexpr int pair_cost(int NW) { return 3 * NW; }
 constexpr int kJoin = 8;            // parts of a cut pair read at a time
-constexpr int kLeastTiles = 16;     // fewest tiles worth a block of their own
+constexpr int kLeastTiles = 4;      // fewest tiles of a warp worth a worker of their own
 constexpr float kOffset = 14.0f;    // probabilities enter fp16 times 2^14
 constexpr float kSlack = 1.5f;      // log2 by which a row's reference may lag its maximum
 constexpr float kTiny = 1e-37f;     // least factor of a score: -inf times 0 would be NaN
@@ -90,20 +92,20 @@ __device__ __forceinline__ int64_t div_by(int64_t x, int64_t y) {
 
 // ------------------------------------------------------------------- plan
 
-// Pairs of a request, and their weight: each its tiles and kPairCost.
+// Pairs of a request, and their weight: each its tiles and its fixed cost.
 __device__ __forceinline__ int64_t pairs_of(int64_t rows, int Hkv, int G, int R) {
   return ceil_div(rows * G, R) * Hkv;
 }
-__device__ __forceinline__ int64_t weight_of(int64_t pairs, int n, int TK) {
-  return pairs * (ceil_div(n, TK) + kPairCost);
+__device__ __forceinline__ int64_t weight_of(int64_t pairs, int n, int TK, int cost) {
+  return pairs * (ceil_div(n, TK) + cost);
 }
 
-// A block's share of all weight.  Where there are more blocks than pairs, one
-// below kLeastTiles would only add joins, and one above the pairs' mean would
-// put two of them into one block.
-__device__ __forceinline__ int64_t share_of(int64_t total, int64_t pairs, int grid) {
-  const int64_t share = div_by(total + grid - 1, grid), mean = div_by(total + pairs - 1, pairs);
-  int64_t least = kPairCost + kLeastTiles;
+// A worker's share of all weight.  Where there are more workers than pairs, one
+// below kLeastTiles a warp would only add joins, and one above the pairs' mean
+// would put two of them into one worker.
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t pairs, int workers, int NW) {
+  const int64_t share = div_by(total + workers - 1, workers), mean = div_by(total + pairs - 1, pairs);
+  int64_t least = pair_cost(NW) + NW * kLeastTiles;
   if (least > mean) least = mean;
   return share > least ? share : least;
 }
@@ -112,7 +114,7 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int64_t pairs, int gr
 // every block to sum them.
 __global__ void __launch_bounds__(1024)
     k_kv_plan(int64_t B, const int64_t* off, int64_t total_q, const int32_t* lens, int Hkv, int G,
-              int64_t most, int R, int TK, int64_t* prefix, unsigned* status) {
+              int64_t most, int R, int TK, int cost, int64_t* prefix, unsigned* status) {
   __shared__ int64_t part[32];
   __shared__ unsigned long long all_pairs;
   if (threadIdx.x == 0) all_pairs = 0;
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(1024)
     int64_t a, b;
     user_range(off, u, B, total_q, &a, &b, status);
     const int64_t p = pairs_of(b - a, Hkv, G, R);
-    const int64_t w = weight_of(p, kv_len(lens, u, most, status), TK);
+    const int64_t w = weight_of(p, kv_len(lens, u, most, status), TK, cost);
     prefix[u] = w;
     sum += w;
     pairs += p;
@@ -309,13 +311,16 @@ struct Segment {
 };
 
 // ONE: a softmax step's keys lie in one block (block >= SK), under one scale.
-template <typename T, int DH, int MT, bool ONE>
+// NW: warps of a worker, which share a segment's tiles (kWarps), or each take
+// segments of their own (1).
+template <typename T, int DH, int MT, bool ONE, int NW>
 __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     k_kv_attn(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
               const Args a) {
   constexpr bool kSplit = sizeof(T) == 4;  // fp32 rows: operands as two fp16 terms
   constexpr int NQ = kSplit ? 2 : 1;
   constexpr int TK = Tile<DH>::TK, SK = Tile<DH>::SK, S = Tile<DH>::kStages, NG = SK / 16;
+  constexpr int kGroups = kWarps / NW;     // workers of a block
   constexpr int NC = ONE ? 1 : NG;         // scales of a step
   constexpr int R = 16 * MT;
   constexpr int KS = DH / 16;              // k-steps of the score product
@@ -327,13 +332,19 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kWarps][S];
   __shared__ float2 ml[kWarps][R];
-  __shared__ int abort_flag, is_last;
+  __shared__ int abort_flag, arrived;
   __shared__ Segment segments[kWarps];
-  __shared__ int64_t warp_sum[kWarps], warp_pairs[kWarps], found[2];
+  __shared__ int64_t warp_sum[kWarps], warp_pairs[kWarps], found[kGroups][2];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1,024-byte aligned: the swizzle's period
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  const int group = warp / NW, gw = warp % NW, gt = threadIdx.x % (NW * 32);  // worker, warp and thread in it
+  const int worker = blockIdx.x * kGroups + group, workers = gridDim.x * kGroups;
+  auto sync = [&] {                        // of a worker
+    if (NW == 1) __syncwarp();
+    else __syncthreads();
+  };
   uint8_t* ring = smem + warp * Tile<DH>::kRing;
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -354,8 +365,8 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   if (a.prefix) {
     total = a.prefix[a.B];
     if (total == 0) return;
-    share = share_of(total, a.prefix[a.B + 1], gridDim.x);
-    const int64_t at = share * blockIdx.x;
+    share = share_of(total, a.prefix[a.B + 1], workers, NW);
+    const int64_t at = share * worker;
     if (at >= total) return;
     u = find_request(a.prefix, a.B, at);
     before = a.prefix[u];
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       int64_t x, y;
       user_range(a.off, v, a.B, a.total_q, &x, &y, a.status);
       const int64_t p = pairs_of(y - x, a.Hkv, a.G, R);
-      sum += weight_of(p, kv_len(a.lens, v, most, a.status), TK);
+      sum += weight_of(p, kv_len(a.lens, v, most, a.status), TK, pair_cost(NW));
       count += p;
     }
     int64_t x = sum;
@@ -388,28 +399,33 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       pairs += warp_pairs[w];
     }
     if (total == 0) return;
-    share = share_of(total, pairs, gridDim.x);
-    const int64_t at = share * blockIdx.x;
-    if (at >= total) return;
-    if (from <= at && at < from + sum) {
-      int64_t v = u0;
-      for (;; ++v) {
-        int64_t p, q;
-        user_range(a.off, v, a.B, a.total_q, &p, &q, a.status);
-        const int64_t w = weight_of(pairs_of(q - p, a.Hkv, a.G, R), kv_len(a.lens, v, most, a.status), TK);
-        if (at < from + w) break;
-        from += w;
+    share = share_of(total, pairs, workers, NW);
+    if (share * blockIdx.x * kGroups >= total) return;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int64_t at = share * (blockIdx.x * kGroups + i);
+      if (from <= at && at < from + sum) {
+        int64_t v = u0, f = from;
+        for (;; ++v) {
+          int64_t p, q;
+          user_range(a.off, v, a.B, a.total_q, &p, &q, a.status);
+          const int64_t w = weight_of(pairs_of(q - p, a.Hkv, a.G, R), kv_len(a.lens, v, most, a.status), TK,
+                                      pair_cost(NW));
+          if (at < f + w) break;
+          f += w;
+        }
+        found[i][0] = v;
+        found[i][1] = f;
       }
-      found[0] = v;
-      found[1] = from;
     }
     __syncthreads();
-    u = found[0];
-    before = found[1];
+    if (share * worker >= total) return;   // the whole worker
+    u = found[group][0];
+    before = found[group][1];
   }
   volatile Segment& sg = segments[warp];
   if (lane == 0) {
-    const int64_t pos = share * blockIdx.x;
+    const int64_t pos = share * worker;
     sg.pos = pos;
     sg.pos_end = pos + share < total ? pos + share : total;
     sg.share = share;
@@ -435,19 +451,19 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     for (;;) {
       user_range(a.off, u, a.B, a.total_q, &q0, &q1, a.status);
       n = kv_len(a.lens, u, most, a.status);
-      w_request = weight_of(pairs_of(q1 - q0, a.Hkv, a.G, R), n, TK);
+      w_request = weight_of(pairs_of(q1 - q0, a.Hkv, a.G, R), n, TK, pair_cost(NW));
       if (pos < before + w_request) break;
       before += w_request;
       ++u;
     }
     const int m_rows = (int)(q1 - q0);
     const int rts = (int)ceil_div((int64_t)m_rows * a.G, R);
-    const int64_t w_pair = (n + TK - 1) / TK + kPairCost;
+    const int64_t w_pair = (n + TK - 1) / TK + pair_cost(NW);
     const int64_t pair = div_by(pos - before, w_pair);
     const int64_t pair_pos = before + pair * w_pair;         // where the pair begins
     const int64_t seg_end = pair_pos + w_pair < pos_end ? pair_pos + w_pair : pos_end;
     const int h = (int)((uint32_t)pair / (uint32_t)rts), rt = (int)pair - h * rts;
-    int t0 = (int)(pos - pair_pos) - kPairCost, t1 = (int)(seg_end - pair_pos) - kPairCost;
+    int t0 = (int)(pos - pair_pos) - pair_cost(NW), t1 = (int)(seg_end - pair_pos) - pair_cost(NW);
     if (t0 < 0) t0 = 0;
     if (t1 < 0) t1 = 0;
 
@@ -508,13 +524,13 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     }
 
     // ---- table entries and scales of 32 / nb tiles ahead, one block per lane
-    const int count = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
+    const int count = t1 - t0 > gw ? (t1 - t0 - gw + NW - 1) / NW : 0;
     auto load_batch = [&](int first, int& ent, float2& sc) {
       const int j = first + lane / nb;
       ent = -1;
       sc = make_float2(-1.0f, 0.0f);     // a negative key scale hides the block
       if (j < count && lane < batch * nb) {
-        const int col = (((t0 + warp + j * kWarps) * TK) >> a.log_block) + lane % nb;
+        const int col = (((t0 + gw + j * NW) * TK) >> a.log_block) + lane % nb;
         if (col < (sg.n + bs - 1) >> a.log_block) {
           const int b = a.table[sg.u * a.max_blocks + col];
           if (b >= 0 && b < a.n_blocks) {
@@ -544,7 +560,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         mbar_arrive_expect_tx(&full[warp][st], (uint32_t)__popc(live) * box_bytes * 2);
       __syncwarp();
       if (ok) {
-        const int row = bs >= TK ? (((t0 + warp + j * kWarps) * TK) & (bs - 1)) * DH / 128 : 0;
+        const int row = bs >= TK ? (((t0 + gw + j * NW) * TK) & (bs - 1)) * DH / 128 : 0;
         uint8_t* dst = ring + st * 2 * Tile<DH>::kBytes + lane * box_bytes;
         const int z = b * a.Hkv + h;
         asm volatile(
@@ -628,7 +644,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
 
 #pragma unroll 1
       for (int sub = 0; sub < TK; sub += SK) {
-        const int key0 = (t0 + warp + j * kWarps) * TK + sub;
+        const int key0 = (t0 + gw + j * NW) * TK + sub;
         if (key0 >= lim_high) break;
         const uint32_t flip = ((sub * DH >> 7) & 7) << 4;  // of the step's first row (0 but for DH 16)
 
@@ -839,14 +855,14 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
               make_float4(out[d], out[d + 1], out[d + 2], out[d + 3]);
       }
     }
-    __syncthreads();
+    sync();
 
-    const int first_cta = (int)div_by(sg.pair_pos, sg.share);
-    const int last_cta = (int)div_by(sg.pair_pos + sg.w_pair - 1, sg.share);
+    const int first = (int)div_by(sg.pair_pos, sg.share);
+    const int last = (int)div_by(sg.pair_pos + sg.w_pair - 1, sg.share);
     const int out_rows = sg.rows;
     const int64_t q_first = sg.q0;
-    const bool whole = first_cta == last_cta;
-    float* part = a.part + (int64_t)(2 * blockIdx.x + (blockIdx.x == first_cta ? 1 : 0)) * (R * DH + 2 * R);
+    const bool whole = first == last;
+    float* part = a.part + (int64_t)(2 * worker + (worker == first ? 1 : 0)) * (R * DH + 2 * R);
     auto store = [&](int r, int d, float4 v, float top, float sum) {
       const int rr = sg.r_base + r, qi = query_of(rr);
       const int64_t at = (q_first + qi) * a.Hq + h * a.G + rr - qi * a.G;
@@ -858,26 +874,26 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       }
       if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - kOffset) * kLn2;
     };
-    for (int i = threadIdx.x; i < out_rows * (DH / 4); i += kWarps * 32) {
+    for (int i = gt; i < out_rows * (DH / 4); i += NW * 32) {
       const int r = i / (DH / 4), d = i % (DH / 4) * 4;
-      float2 x[kWarps];
+      float2 x[NW];
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        x[w] = ml[w][r];
+      for (int w = 0; w < NW; ++w) {
+        x[w] = ml[group * NW + w][r];
         top = fmaxf(top, x[w].x);
       }
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < NW; ++w) {
         x[w].y *= ex2(x[w].x - (top == -INFINITY ? 0.0f : top));
         sum += x[w].y;
       }
       const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>((float*)(smem + w * Tile<DH>::kRing) + r * DH + d);
+      for (int w = 0; w < NW; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>((float*)(smem + (group * NW + w) * Tile<DH>::kRing) + r * DH + d);
         const float k = x[w].y * by;
         v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
       }
@@ -891,26 +907,33 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     if (!whole) {
       // the last block to arrive joins the pair's parts in the blocks' order
       __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) is_last = atomicAdd(a.tickets + first_cta, 1) == last_cta - first_cta;
-      __syncthreads();
-      if (is_last) {
-        if (threadIdx.x == 0) a.tickets[first_cta] = 0;
+      sync();
+      int before_me = 0;
+      if (gt == 0) before_me = atomicAdd(a.tickets + first, 1);
+      if (NW == 1) {
+        before_me = __shfl_sync(0xffffffffu, before_me, 0);
+      } else {
+        if (gt == 0) arrived = before_me;
+        __syncthreads();
+        before_me = arrived;
+      }
+      if (before_me == last - first) {
+        if (gt == 0) a.tickets[first] = 0;
         __threadfence();
         const int64_t pitch = R * DH + 2 * R;
-        auto slot = [&](int c) { return a.part + (2 * (int64_t)c + (c == first_cta ? 1 : 0)) * pitch; };
-        for (int i = threadIdx.x; i < out_rows * (DH / 4); i += kWarps * 32) {
+        auto slot = [&](int c) { return a.part + (2 * (int64_t)c + (c == first ? 1 : 0)) * pitch; };
+        for (int i = gt; i < out_rows * (DH / 4); i += NW * 32) {
           const int r = i / (DH / 4), d = i % (DH / 4) * 4;
           float top = -INFINITY, sum = 0.0f;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c0 = first_cta; c0 <= last_cta; c0 += kJoin) {
+          for (int c0 = first; c0 <= last; c0 += kJoin) {
             float2 x[kJoin];             // kJoin parts in flight
             float4 y[kJoin];
 #pragma unroll
             for (int c = 0; c < kJoin; ++c) {
               x[c] = make_float2(-INFINITY, 0.0f);
               y[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (c0 + c <= last_cta) {
+              if (c0 + c <= last) {
                 x[c] = __ldcg(reinterpret_cast<const float2*>(slot(c0 + c) + R * DH + 2 * r));
                 y[c] = __ldcg(reinterpret_cast<const float4*>(slot(c0 + c) + r * DH + d));
               }
@@ -936,7 +959,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       }
     }
     fence_proxy_async_smem();            // the ring's next writes are TMA's
-    __syncthreads();
+    sync();
     if (lane == 0) sg.pos = sg.seg_end;
     __syncwarp();
   }
@@ -951,9 +974,9 @@ int pair_rows(const lime_kv_dims& D, int64_t rows_per_head) {
   return D.dtype == LIME_BF16 && D.dh <= 64 && rows_per_head > 16 ? 32 : 16;
 }
 
-template <typename T, int DH, int MT, bool ONE>
+template <typename T, int DH, int MT, bool ONE, int NW>
 int launch(Args a, CUtensorMap mk, CUtensorMap mv, int64_t* prefix, cudaStream_t st) {
-  auto kernel = k_kv_attn<T, DH, MT, ONE>;
+  auto kernel = k_kv_attn<T, DH, MT, ONE, NW>;
   const size_t smem = kWarps * Tile<DH>::kRing + 1024;
   static int per_sm[64] = {0};
   int dev = 0;
@@ -974,7 +997,7 @@ int launch(Args a, CUtensorMap mk, CUtensorMap mv, int64_t* prefix, cudaStream_t
     a.prefix = prefix;
     const int rc = launch_pdl(k_kv_plan, dim3(1), dim3(1024), 0, st, 1, a.B, a.off, a.total_q, a.lens,
                               a.Hkv, a.G, (int64_t)a.max_blocks << a.log_block, 16 * MT,
-                              (int)Tile<DH>::TK, prefix, a.status);
+                              (int)Tile<DH>::TK, pair_cost(NW), prefix, a.status);
     if (rc) return rc;
   }
   return launch_pdl(kernel, dim3(grid), dim3(kWarps * 32), smem, st, 1, mk, mv, a);
@@ -982,12 +1005,12 @@ int launch(Args a, CUtensorMap mk, CUtensorMap mv, int64_t* prefix, cudaStream_t
 
 }  // namespace
 
-size_t kv_ticket_bytes() { return kMaxCtas * sizeof(int); }
+size_t kv_ticket_bytes() { return kMaxWorkers * sizeof(int); }
 
 size_t kv_attention_ws_bytes(const lime_kv_dims& D, int64_t B, int64_t total_q) {
   if (total_q == 0) return 0;
   const size_t prefix = B > kInlineRequests ? ((size_t)(B + 2) * 8 + 255) / 256 * 256 : 0;
-  return prefix + 2 * kMaxCtas * part_floats(D.dh <= 64 ? 32 : 16, D.dh) * 4;
+  return prefix + 2 * kMaxWorkers * part_floats(D.dh <= 64 ? 32 : 16, D.dh) * 4;
 }
 
 int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, const int64_t* off,
@@ -1017,10 +1040,18 @@ int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, c
   a.log_g = (G & (G - 1)) ? -1 : 0;
   while (a.log_g >= 0 && 1 << a.log_g < G) ++a.log_g;
   a.scale_log2 = fabsf(sm_scale) * kLog2e, a.negative = sm_scale < 0.0f, a.causal = causal;
-#define RUN(T, DH, MT)                                                 \
-  return D.block >= Tile<DH>::SK                                       \
-             ? launch<T, DH, MT, true>(a, mk, mv, prefix, st) \
-             : launch<T, DH, MT, false>(a, mk, mv, prefix, st)
+  // Workers of one warp where every warp of the GPU gets a pair: their segments
+  // are longer, and one warp's start and end run beside the others' tiles.
+  const int64_t pairs = ceil_div(total_q * G, R) * D.Hkv;
+  const bool own = pairs >= (int64_t)num_sms() * 2 * kWarps;
+#define RUN2(T, DH, MT, ONE)                                        \
+  return own ? launch<T, DH, MT, ONE, 1>(a, mk, mv, prefix, st)     \
+             : launch<T, DH, MT, ONE, kWarps>(a, mk, mv, prefix, st)
+#define RUN(T, DH, MT)                        \
+  do {                                        \
+    if (D.block >= Tile<DH>::SK) RUN2(T, DH, MT, true); \
+    RUN2(T, DH, MT, false);                   \
+  } while (0)
   if (D.dtype == LIME_BF16) {
     if (D.dh == 16) { if (R == 32) RUN(bf16, 16, 2); RUN(bf16, 16, 1); }
     if (D.dh == 32) { if (R == 32) RUN(bf16, 32, 2); RUN(bf16, 32, 1); }
@@ -1031,6 +1062,7 @@ int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, c
   if (D.dh == 32) RUN(float, 32, 1);
   if (D.dh == 64) RUN(float, 64, 1);
   RUN(float, 128, 1);
+#undef RUN2
 #undef RUN
 }
 
