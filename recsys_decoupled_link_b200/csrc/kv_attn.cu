@@ -17,30 +17,20 @@
 // into the fragment.  Which key a fragment's column stands for, and which dims
 // a lane holds, are free as long as both products agree; KeyMap picks them so
 // that every shared-memory read is a wide one without bank conflicts.
-#include <math.h>
-
-#include "lime_fast.cuh"
-#include "lime_kv.cuh"
-#include "sm100.cuh"
+#include "kv_attn.cuh"
 
 namespace lime {
 
-using namespace sm100;
+using namespace kv;
 
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kMaxCtas = 640;       // most blocks of the persistent grid
-constexpr int kMaxWorkers = kWarps * kMaxCtas;
-// A pair's fixed cost, in tiles of a worker of NW warps.
-__host__ __device__ constexpr int pair_cost(int NW) { return 3 * NW; }
-constexpr int kJoin = 8;            // parts of a cut pair read at a time
-constexpr int kLeastTiles = 4;      // fewest tiles of a warp worth a worker of their own
-constexpr float kOffset = 14.0f;    // probabilities enter fp16 times 2^14
-constexpr float kSlack = 1.5f;      // log2 by which a row's reference may lag its maximum
-constexpr float kTiny = 1e-37f;     // least factor of a score: -inf times 0 would be NaN
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+
+// How a worker of NW warps divides the work: a pair's fixed cost in its tiles,
+// and the fewest tiles worth a worker of their own.
+template <int NW> constexpr int kPairCost = 3 * NW;
+template <int NW> constexpr int kLeast = 7 * NW;
 
 // Per head dim: keys of a warp's tile (one ring stage), keys of one softmax
 // step, stages of the ring.
@@ -52,69 +42,14 @@ template <int DH> struct Tile {
   static constexpr int kRing = kStages * 2 * kBytes; // per warp
 };
 
-constexpr int kInlineRequests = 2048;  // most requests whose weights every block sums itself
-
-struct Args {
-  const void* Q;
-  int64_t ldq;
-  const int64_t* off;
-  const int32_t* table;
-  const int32_t* lens;
-  const float2* scale;
-  const int64_t* prefix;  // [B + 2] weight before each request, then the
-                          // number of pairs (NULL: summed by every block)
-  int* tickets;           // [grid] zero between calls
-  float* part;            // [2 * grid] partial results
-  void* O;
-  float* lse;
-  unsigned* status;
-  int64_t B, total_q, n_blocks;
-  int Hq, Hkv, G, max_blocks;
-  int log_block;
-  int log_g;         // of G, or -1 where it is no power of two
-  float scale_log2;  // |sm_scale| log2 e
-  bool negative;     // sm_scale < 0
-  bool causal;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// x / y, in 32 bits where they suffice (a 64-bit division takes most of a
-// microsecond of a segment's start).
-__device__ __forceinline__ int64_t div_by(int64_t x, int64_t y) {
-  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
-  return x / y;
-}
 
 // ------------------------------------------------------------------- plan
-
-// Pairs of a request, and their weight: each its tiles and its fixed cost.
-__device__ __forceinline__ int64_t pairs_of(int64_t rows, int Hkv, int G, int R) {
-  return ceil_div(rows * G, R) * Hkv;
-}
-__device__ __forceinline__ int64_t weight_of(int64_t pairs, int n, int TK, int cost) {
-  return pairs * (ceil_div(n, TK) + cost);
-}
-
-// A worker's share of all weight.  Where there are more workers than pairs, one
-// below kLeastTiles a warp would only add joins, and one above the pairs' mean
-// would put two of them into one worker.
-__device__ __forceinline__ int64_t share_of(int64_t total, int64_t pairs, int workers, int NW) {
-  const int64_t share = div_by(total + workers - 1, workers), mean = div_by(total + pairs - 1, pairs);
-  int64_t least = pair_cost(NW) + NW * kLeastTiles;
-  if (least > mean) least = mean;
-  return share > least ? share : least;
-}
 
 // Prefix sums of the requests' weights, where there are too many requests for
 // every block to sum them.
 __global__ void __launch_bounds__(1024)
-    k_kv_plan(int64_t B, const int64_t* off, int64_t total_q, const int32_t* lens, int Hkv, int G,
-              int64_t most, int R, int TK, int cost, int64_t* prefix, unsigned* status) {
+    k_kv_plan(int64_t B, const int64_t* off, int64_t total_q, const int32_t* lens, int G, int64_t most,
+              Cut cut, int64_t* prefix, unsigned* status) {
   __shared__ int64_t part[32];
   __shared__ unsigned long long all_pairs;
   if (threadIdx.x == 0) all_pairs = 0;
@@ -128,8 +63,8 @@ __global__ void __launch_bounds__(1024)
   for (int64_t u = u0; u < u1; ++u) {
     int64_t a, b;
     user_range(off, u, B, total_q, &a, &b, status);
-    const int64_t p = pairs_of(b - a, Hkv, G, R);
-    const int64_t w = weight_of(p, kv_len(lens, u, most, status), TK, cost);
+    const int64_t p = cut.pairs(b - a, G);
+    const int64_t w = p * cut.weight(kv_len(lens, u, most, status));
     prefix[u] = w;
     sum += w;
     pairs += p;
@@ -165,22 +100,6 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// The request whose weights hold position s: the largest u with prefix[u] <= s
-// (a warp probes 32 places at a time).
-__device__ __forceinline__ int64_t find_request(const int64_t* prefix, int64_t B, int64_t s) {
-  const int lane = threadIdx.x & 31;
-  int64_t lo = 0, hi = B;  // answer in [lo, hi)
-  while (hi - lo > 1) {
-    const int64_t step = ceil_div(hi - lo, 32);
-    const int64_t p = lo + step * lane;
-    const bool ok = p < hi && prefix[p] <= s;
-    const int n = __popc(__ballot_sync(0xffffffffu, ok));  // n >= 1
-    lo += step * (n - 1);
-    hi = lo + step < hi ? lo + step : hi;
-  }
-  return lo;
-}
-
 // -------------------------------------------------------------- fragments
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -197,55 +116,6 @@ __device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, uint
       "{%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-// Two fp32 values to an instruction.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The same, the largest finite fp16 in place of an overflow: a probability is at
-// most 2^(kOffset + kSlack), unless scores beyond 2^22 cost its exponent half a
-// unit.
-__device__ __forceinline__ uint32_t half2_sat(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// {1024 + b0, 1024 + b1} - 1152 of two biased bytes (code + 128) picked by SEL.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
-  const uint32_t m = __byte_perm(w, 0x64646464u, SEL);
-  const uint32_t bias = 0x64806480u;
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&m),
-                            *reinterpret_cast<const __half2*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Byte offset inside a tile, through the 128-byte swizzle the TMA applies.
@@ -297,19 +167,6 @@ constexpr int min_blocks() {
   return DH <= 32 ? (MT == 2 ? 2 : 4) : DH == 64 ? (MT == 2 ? 2 : 3) : (sizeof(T) == 2 ? 3 : 2);
 }
 
-// What a segment's start and end know and its tile loop hardly needs: kept in
-// shared memory, a copy per warp, for the registers it would hold meanwhile.
-struct Segment {
-  int64_t pos, pos_end;       // this block's place in the weights, and its end
-  int64_t share;              // of every block
-  int64_t u, before;          // request, and the weight before it
-  int64_t pair_pos, seg_end;  // where the pair begins and the segment ends
-  int64_t q0;                 // the request's first query row
-  int n, m_rows;              // its cached and its query rows
-  int r_base, rows;           // the pair's rows (query, head of the group)
-  int w_pair;
-};
-
 // ONE: a softmax step's keys lie in one block (block >= SK), under one scale.
 // NW: warps of a worker, which share a segment's tiles (kWarps), or each take
 // segments of their own (1).
@@ -334,13 +191,13 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   __shared__ float2 ml[kWarps][R];
   __shared__ int abort_flag, arrived;
   __shared__ Segment segments[kWarps];
-  __shared__ int64_t warp_sum[kWarps], warp_pairs[kWarps], found[kGroups][2];
+  __shared__ LocateSmem<kWarps, kGroups> locate_smem;
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1,024-byte aligned: the swizzle's period
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int group = warp / NW, gw = warp % NW, gt = threadIdx.x % (NW * 32);  // worker, warp and thread in it
-  const int worker = blockIdx.x * kGroups + group, workers = gridDim.x * kGroups;
+  const int worker = blockIdx.x * kGroups + group;
   auto sync = [&] {                        // of a worker
     if (NW == 1) __syncwarp();
     else __syncthreads();
@@ -358,82 +215,21 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   pdl_launch();
   pdl_wait();
 
-  // where this block's share begins: request u, whose weights begin at before
-  const int bs = 1 << a.log_block;
-  const int64_t most = (int64_t)a.max_blocks << a.log_block;
-  int64_t u, before, total, share;
-  if (a.prefix) {
-    total = a.prefix[a.B];
-    if (total == 0) return;
-    share = share_of(total, a.prefix[a.B + 1], workers, NW);
-    const int64_t at = share * worker;
-    if (at >= total) return;
-    u = find_request(a.prefix, a.B, at);
-    before = a.prefix[u];
-  } else {
-    const int per = (int)ceil_div(a.B, kWarps * 32);
-    const int64_t u0 = (int64_t)per * threadIdx.x, u1 = u0 + per < a.B ? u0 + per : a.B;
-    int64_t sum = 0, count = 0;
-    for (int64_t v = u0; v < u1; ++v) {
-      int64_t x, y;
-      user_range(a.off, v, a.B, a.total_q, &x, &y, a.status);
-      const int64_t p = pairs_of(y - x, a.Hkv, a.G, R);
-      sum += weight_of(p, kv_len(a.lens, v, most, a.status), TK, pair_cost(NW));
-      count += p;
-    }
-    int64_t x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-      count += __shfl_xor_sync(0xffffffffu, count, o);
-    }
-    if (lane == 31) warp_sum[warp] = x, warp_pairs[warp] = count;
-    __syncthreads();
-    total = 0;
-    int64_t from = x - sum, pairs = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) from += warp_sum[w];
-      total += warp_sum[w];
-      pairs += warp_pairs[w];
-    }
-    if (total == 0) return;
-    share = share_of(total, pairs, workers, NW);
-    if (share * blockIdx.x * kGroups >= total) return;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int64_t at = share * (blockIdx.x * kGroups + i);
-      if (from <= at && at < from + sum) {
-        int64_t v = u0, f = from;
-        for (;; ++v) {
-          int64_t p, q;
-          user_range(a.off, v, a.B, a.total_q, &p, &q, a.status);
-          const int64_t w = weight_of(pairs_of(q - p, a.Hkv, a.G, R), kv_len(a.lens, v, most, a.status), TK,
-                                      pair_cost(NW));
-          if (at < f + w) break;
-          f += w;
-        }
-        found[i][0] = v;
-        found[i][1] = f;
-      }
-    }
-    __syncthreads();
-    if (share * worker >= total) return;   // the whole worker
-    u = found[group][0];
-    before = found[group][1];
-  }
+  const Cut cut = {a.Hkv, R, TK, kPairCost<NW>, kLeast<NW>};
+  Place place;
+  if (!locate<kWarps, kGroups>(a, cut, locate_smem, group, &place)) return;
   volatile Segment& sg = segments[warp];
   if (lane == 0) {
-    const int64_t pos = share * worker;
+    const int64_t pos = place.share * worker;
     sg.pos = pos;
-    sg.pos_end = pos + share < total ? pos + share : total;
-    sg.share = share;
-    sg.u = u;
-    sg.before = before;
+    sg.pos_end = pos + place.share < place.total ? pos + place.share : place.total;
+    sg.share = place.share;
+    sg.u = place.u;
+    sg.before = place.before;
   }
   __syncwarp();
 
+  const int bs = 1 << a.log_block;
   const int nb = bs >= TK ? 1 : TK / bs;   // blocks of a tile
   const int box_rows = bs >= TK ? TK : bs;
   const uint32_t box_bytes = (uint32_t)box_rows * DH;
@@ -445,47 +241,12 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   uint32_t stage = 0, phase = 0;           // of the ring; phase: one bit per stage
 
   while (sg.pos < sg.pos_end) {
-    const int64_t pos = sg.pos, pos_end = sg.pos_end;
-    int64_t u = sg.u, before = sg.before, q0, q1, w_request;
-    int n;
-    for (;;) {
-      user_range(a.off, u, a.B, a.total_q, &q0, &q1, a.status);
-      n = kv_len(a.lens, u, most, a.status);
-      w_request = weight_of(pairs_of(q1 - q0, a.Hkv, a.G, R), n, TK, pair_cost(NW));
-      if (pos < before + w_request) break;
-      before += w_request;
-      ++u;
-    }
-    const int m_rows = (int)(q1 - q0);
-    const int rts = (int)ceil_div((int64_t)m_rows * a.G, R);
-    const int64_t w_pair = (n + TK - 1) / TK + pair_cost(NW);
-    const int64_t pair = div_by(pos - before, w_pair);
-    const int64_t pair_pos = before + pair * w_pair;         // where the pair begins
-    const int64_t seg_end = pair_pos + w_pair < pos_end ? pair_pos + w_pair : pos_end;
-    const int h = (int)((uint32_t)pair / (uint32_t)rts), rt = (int)pair - h * rts;
-    int t0 = (int)(pos - pair_pos) - pair_cost(NW), t1 = (int)(seg_end - pair_pos) - pair_cost(NW);
-    if (t0 < 0) t0 = 0;
-    if (t1 < 0) t1 = 0;
-
-    auto query_of = [&](int r) { return a.log_g >= 0 ? r >> a.log_g : r / a.G; };  // of row r
-    // the rows' limits: row r sees keys below limit(r)
-    const int r_base = rt * R, rows = m_rows * a.G - r_base < R ? m_rows * a.G - r_base : R;
-    __syncwarp();
-    if (lane == 0) {
-      sg.u = u, sg.before = before;
-      sg.pair_pos = pair_pos, sg.seg_end = seg_end, sg.q0 = q0;
-      sg.n = n, sg.m_rows = m_rows, sg.r_base = r_base, sg.rows = rows;
-      sg.w_pair = (int)w_pair;
-    }
-    __syncwarp();
-    auto limit_of = [&](int r) {
-      if (!a.causal) return (int)sg.n;
-      const int lim = sg.n - sg.m_rows + query_of(sg.r_base + r) + 1;
-      return lim < 0 ? 0 : lim;
-    };
-    const int lim_low = limit_of(0), lim_high = limit_of(rows - 1);
+    const Head head = next_segment(a, cut, sg);
+    const int h = head.h, t0 = head.t0, rows = sg.rows, r_base = sg.r_base;
+    const int64_t q0 = sg.q0;
+    const int lim_low = limit_of(a, sg, 0), lim_high = limit_of(a, sg, rows - 1);
     const int t_live = (lim_high + TK - 1) / TK;
-    if (t1 > t_live) t1 = t_live;
+    const int t1 = head.t1 < t_live ? head.t1 : t_live;
 
     float o[MT][NT][4], m[MT][2], vref = 0.0f;
     uint64_t l[MT][2];                   // sums of the even and the odd columns
@@ -510,7 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
 #pragma unroll
         for (int i = 0; i < NV; ++i) raw[mt][hf][i] = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-          const int rr = r_base + r, qi = query_of(rr);
+          const int rr = r_base + r, qi = query_of(a, rr);
           const T* src = (const T*)a.Q + (q0 + qi) * a.ldq + (h * a.G + rr - qi * a.G) * DH + E * t;
           if constexpr (E * sizeof(T) >= 16) {
 #pragma unroll
@@ -527,20 +288,8 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     const int count = t1 - t0 > gw ? (t1 - t0 - gw + NW - 1) / NW : 0;
     auto load_batch = [&](int first, int& ent, float2& sc) {
       const int j = first + lane / nb;
-      ent = -1;
-      sc = make_float2(-1.0f, 0.0f);     // a negative key scale hides the block
-      if (j < count && lane < batch * nb) {
-        const int col = (((t0 + gw + j * NW) * TK) >> a.log_block) + lane % nb;
-        if (col < (sg.n + bs - 1) >> a.log_block) {
-          const int b = a.table[sg.u * a.max_blocks + col];
-          if (b >= 0 && b < a.n_blocks) {
-            ent = b;
-            sc = a.scale[(int64_t)b * a.Hkv + h];
-          } else {
-            raise_flag(a.status, LIME_FLAG_BAD_BLOCK);
-          }
-        }
-      }
+      const int col = (((t0 + gw + j * NW) * TK) >> a.log_block) + lane % nb;
+      load_entry(a, sg, h, j < count ? col : INT32_MAX, &ent, &sc);
     };
     int ent0, ent1;
     float2 sc0, sc1;
@@ -606,13 +355,8 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         for (int d = 0; d < E; ++d) top = fmaxf(top, fabsf(x[d]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e <= top < 2^(e+1): times 2^(14-e), as two exact factors
-        const int exp = (__float_as_int(top) >> 23) & 255;
-        const int shift = 14 + 127 - (exp < 254 ? exp : 254);
-        const int e1 = shift >> 1, e2 = shift - e1;
-        const float s1 = __int_as_float((127 + e1) << 23) * (a.negative ? -1.0f : 1.0f);
-        const float s2 = __int_as_float((127 + e2) << 23);
-        c_row[mt][hf] = a.scale_log2 * __int_as_float((127 - e1) << 23) * __int_as_float((127 - e2) << 23);
+        float s1, s2;
+        row_scale(a, top, &s1, &s2, &c_row[mt][hf]);
 #pragma unroll
         for (int w = 0; w < KS; ++w) {
           float y[4];
@@ -648,6 +392,39 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         if (key0 >= lim_high) break;
         const uint32_t flip = ((sub * DH >> 7) & 7) << 4;  // of the step's first row (0 but for DH 16)
 
+        // ---- the blocks' scales; hidden keys
+        float kg[NC], vg[NC];
+        bool hidden = false;
+        float vmax = 0.0f;
+#pragma unroll
+        for (int x = 0; x < NC; ++x) {
+          const int src = (j - base) * nb + (nb > 1 ? (sub + x * 16) >> a.log_block : 0);
+          kg[x] = __shfl_sync(0xffffffffu, sc0.x, src);
+          vg[x] = __shfl_sync(0xffffffffu, sc0.y, src);
+          hidden |= kg[x] < 0.0f;
+          vmax = fmaxf(vmax, vg[x]);
+        }
+        // the value unit grows with the scales seen (rarely after the first)
+        if (vmax > vref) {
+          const float keep = vref / vmax;
+          vref = vmax;
+          const uint64_t keep2 = pack2(keep, keep);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                unpack2(mul2(pack2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]), keep2), o[mt][i][2 * hf],
+                        o[mt][i][2 * hf + 1]);
+        }
+        // probabilities carry their block's value scale over the unit: log2 of
+        // the ratio joins the exponent, at least -60 (what is smaller adds
+        // nothing); the sum takes it out again
+        float lr[NC], inv[NC];
+#pragma unroll
+        for (int x = 0; x < NC; ++x) unit_log2(vg[x], vref, &lr[x], &inv[x]);
+
         // ---- scores
         float s[MT][2 * NG][4];
 #pragma unroll
@@ -671,25 +448,13 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
           }
         }
 
-        // ---- the blocks' scales; hidden keys
-        float kg[NC], vg[NC];
-        bool hidden = false;
-        float vmax = 0.0f;
-#pragma unroll
-        for (int x = 0; x < NC; ++x) {
-          const int src = (j - base) * nb + (nb > 1 ? (sub + x * 16) >> a.log_block : 0);
-          kg[x] = __shfl_sync(0xffffffffu, sc0.x, src);
-          vg[x] = __shfl_sync(0xffffffffu, sc0.y, src);
-          hidden |= kg[x] < 0.0f;
-          vmax = fmaxf(vmax, vg[x]);
-        }
         if (hidden || key0 + SK > lim_low) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const int r = mt * 16 + hf * 8 + g;
-              const int lim = r < sg.rows ? limit_of(r) : 0;
+              const int lim = r < sg.rows ? limit_of(a, sg, r) : 0;
 #pragma unroll
               for (int x = 0; x < 2 * NG; ++x) {
                 const int key = key0 + (x >> 1) * 16 + (x & 1) * Map::odd;
@@ -704,9 +469,9 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
             if (kg[x] < 0.0f) kg[x] = 1.0f;  // the marker is no factor
         }
 
-        // ---- running maximum (in units of log2) and value unit
+        // ---- running maximum, in units of log2
         float top[MT][2];
-        bool grow = vmax > vref;
+        bool grow = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -724,9 +489,6 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
           }
         }
         if (__any_sync(0xffffffffu, grow)) {
-          const float vnew = fmaxf(vref, vmax);
-          const float vkeep = vnew > 0.0f ? vref / vnew : 0.0f;
-          vref = vnew;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -738,7 +500,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
               const float keep = ex2(m[mt][hf] - (v == -INFINITY ? 0.0f : v));
               m[mt][hf] = v;
               l[mt][hf] = mul2(l[mt][hf], pack2(keep, keep));
-              const uint64_t ok = pack2(keep * vkeep, keep * vkeep);
+              const uint64_t ok = pack2(keep, keep);
 #pragma unroll
               for (int i = 0; i < NT; ++i)
                 unpack2(mul2(pack2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]), ok), o[mt][i][2 * hf],
@@ -747,16 +509,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
           }
         }
 
-        // ---- probabilities times their block's value scale over the unit:
-        // log2 of the ratio joins the exponent, at least -60 (what is smaller
-        // adds nothing); the sum takes it out again
-        float lr[NC], inv[NC];
-#pragma unroll
-        for (int x = 0; x < NC; ++x) {
-          const float ratio = __log2f(__fdividef(vg[x], vref));
-          lr[x] = vref > 0.0f ? (ratio > -60.0f ? ratio : -60.0f) : 0.0f;
-          inv[x] = ex2(-lr[x]);
-        }
+        // ---- probabilities
         uint32_t pf[MT][NG][NQ][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -862,17 +615,10 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     const int out_rows = sg.rows;
     const int64_t q_first = sg.q0;
     const bool whole = first == last;
-    float* part = a.part + (int64_t)(2 * worker + (worker == first ? 1 : 0)) * (R * DH + 2 * R);
+    float* part = part_of<R, DH>(a, worker, first);
     auto store = [&](int r, int d, float4 v, float top, float sum) {
-      const int rr = sg.r_base + r, qi = query_of(rr);
-      const int64_t at = (q_first + qi) * a.Hq + h * a.G + rr - qi * a.G;
-      T* dst = (T*)a.O + at * DH + d;
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(dst) = v;
-      } else {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-      }
-      if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - kOffset) * kLn2;
+      const int rr = sg.r_base + r, qi = query_of(a, rr);
+      store_out<T, DH>(a, (q_first + qi) * a.Hq + h * a.G + rr - qi * a.G, d, v, top, sum);
     };
     for (int i = gt; i < out_rows * (DH / 4); i += NW * 32) {
       const int r = i / (DH / 4), d = i % (DH / 4) * 4;
@@ -920,42 +666,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       if (before_me == last - first) {
         if (gt == 0) a.tickets[first] = 0;
         __threadfence();
-        const int64_t pitch = R * DH + 2 * R;
-        auto slot = [&](int c) { return a.part + (2 * (int64_t)c + (c == first ? 1 : 0)) * pitch; };
-        for (int i = gt; i < out_rows * (DH / 4); i += NW * 32) {
-          const int r = i / (DH / 4), d = i % (DH / 4) * 4;
-          float top = -INFINITY, sum = 0.0f;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c0 = first; c0 <= last; c0 += kJoin) {
-            float2 x[kJoin];             // kJoin parts in flight
-            float4 y[kJoin];
-#pragma unroll
-            for (int c = 0; c < kJoin; ++c) {
-              x[c] = make_float2(-INFINITY, 0.0f);
-              y[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (c0 + c <= last) {
-                x[c] = __ldcg(reinterpret_cast<const float2*>(slot(c0 + c) + R * DH + 2 * r));
-                y[c] = __ldcg(reinterpret_cast<const float4*>(slot(c0 + c) + r * DH + d));
-              }
-            }
-            float best = top;
-#pragma unroll
-            for (int c = 0; c < kJoin; ++c) best = fmaxf(best, x[c].x);
-            const float ref = best == -INFINITY ? 0.0f : best, keep = ex2(top - ref);
-            sum *= keep;
-            v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
-            top = best;
-#pragma unroll
-            for (int c = 0; c < kJoin; ++c) {
-              const float k = x[c].y * ex2(x[c].x - ref);
-              sum += k;
-              v.x = fmaf(k, y[c].x, v.x), v.y = fmaf(k, y[c].y, v.y);
-              v.z = fmaf(k, y[c].z, v.z), v.w = fmaf(k, y[c].w, v.w);
-            }
-          }
-          const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-          store(r, d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by), top, sum);
-        }
+        join_parts<R, DH>(a, first, last, gt, NW * 32, out_rows, [](int) { return true; }, store);
       }
     }
     fence_proxy_async_smem();            // the ring's next writes are TMA's
@@ -963,6 +674,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     if (lane == 0) sg.pos = sg.seg_end;
     __syncwarp();
   }
+  drain_after_timeout(&abort_flag);
 }
 
 // ------------------------------------------------------------------- host
@@ -992,25 +704,30 @@ int launch(Args a, CUtensorMap mk, CUtensorMap mv, int64_t* prefix, cudaStream_t
     per_sm[dev] = n;
   }
   int grid = num_sms() * per_sm[dev];
-  if (grid > kMaxCtas) grid = kMaxCtas;
+  if (grid > kMaxWorkers / kWarps) grid = kMaxWorkers / kWarps;
   if (a.B > kInlineRequests) {
     a.prefix = prefix;
-    const int rc = launch_pdl(k_kv_plan, dim3(1), dim3(1024), 0, st, 1, a.B, a.off, a.total_q, a.lens,
-                              a.Hkv, a.G, (int64_t)a.max_blocks << a.log_block, 16 * MT,
-                              (int)Tile<DH>::TK, pair_cost(NW), prefix, a.status);
-    if (rc) return rc;
+    const Cut cut = {a.Hkv, 16 * MT, Tile<DH>::TK, kPairCost<NW>, kLeast<NW>};
+    if (const int rc = launch_plan(a, cut, prefix, st)) return rc;
   }
   return launch_pdl(kernel, dim3(grid), dim3(kWarps * 32), smem, st, 1, mk, mv, a);
 }
 
 }  // namespace
 
+namespace kv {
+int launch_plan(const Args& a, const Cut& cut, int64_t* prefix, cudaStream_t st) {
+  return launch_pdl(k_kv_plan, dim3(1), dim3(1024), 0, st, 1, a.B, a.off, a.total_q, a.lens, a.G,
+                    (int64_t)a.max_blocks << a.log_block, cut, prefix, a.status);
+}
+}  // namespace kv
+
 size_t kv_ticket_bytes() { return kMaxWorkers * sizeof(int); }
 
 size_t kv_attention_ws_bytes(const lime_kv_dims& D, int64_t B, int64_t total_q) {
   if (total_q == 0) return 0;
   const size_t prefix = B > kInlineRequests ? ((size_t)(B + 2) * 8 + 255) / 256 * 256 : 0;
-  return prefix + 2 * kMaxWorkers * part_floats(D.dh <= 64 ? 32 : 16, D.dh) * 4;
+  return prefix + 2 * kMaxWorkers * part_floats(D.dh <= 64 ? 32 : 16, D.dh) * sizeof(float);
 }
 
 int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, const int64_t* off,
@@ -1023,11 +740,6 @@ int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, c
   int64_t* prefix = (int64_t*)ws;
   const size_t prefix_bytes = B > kInlineRequests ? ((size_t)(B + 2) * 8 + 255) / 256 * 256 : 0;
 
-  CUtensorMap mk, mv;
-  const int box = D.block < TK ? D.block : TK;
-  if (!make_tmap_kv(&mk, kc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh) ||
-      !make_tmap_kv(&mv, vc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh))
-    return LIME_ERR_CUDA;
   Args a = {};
   a.Q = Q, a.ldq = ldq, a.off = off, a.table = table, a.lens = lens;
   a.scale = (const float2*)scale;
@@ -1039,7 +751,12 @@ int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, c
   while (1 << a.log_block < D.block) ++a.log_block;
   a.log_g = (G & (G - 1)) ? -1 : 0;
   while (a.log_g >= 0 && 1 << a.log_g < G) ++a.log_g;
-  a.scale_log2 = fabsf(sm_scale) * kLog2e, a.negative = sm_scale < 0.0f, a.causal = causal;
+  a.scale_log2 = fabsf(sm_scale) * 1.4426950408889634f, a.negative = sm_scale < 0.0f, a.causal = causal;
+  CUtensorMap mk, mv;
+  const int box = D.block < TK ? D.block : TK;
+  if (!make_tmap_kv(&mk, kc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh) ||
+      !make_tmap_kv(&mv, vc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh))
+    return LIME_ERR_CUDA;
   // Workers of one warp where every warp of the GPU gets a pair: their segments
   // are longer, and one warp's start and end run beside the others' tiles.
   const int64_t pairs = ceil_div(total_q * G, R) * D.Hkv;

@@ -363,6 +363,39 @@ def test_attention_links(dtype, dh, Hq, Hkv, l):
     check_attention([l] * len(lens), lens, Hq, Hkv, dh, 64, dtype, strided=True)
 
 
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+@pytest.mark.parametrize("dh,Hq,Hkv,l", [(32, 4, 4, 32), (32, 8, 4, 20), (32, 2, 2, 64), (32, 3, 3, 128), (64, 2, 2, 64),
+                                         (64, 6, 6, 40), (64, 5, 1, 30), (128, 1, 1, 90)])
+def test_attention_many_rows(bs, dh, Hq, Hkv, l):
+    # one to four heads to a tensor-core tile, full and partly filled, one tile of rows and several
+    lens = [70, 0, 1, 200, 64, 129]
+    counts = [l, l, l - 3, l + 7, 3 * l + 1, 0]
+    check_attention(counts, lens, Hq, Hkv, dh, bs, "bf16", strided=True)
+    check_attention(counts, lens, Hq, Hkv, dh, bs, "bf16", causal=True, seed=1)
+
+
+def test_attention_many_rows_split_over_the_gpu():
+    check_attention([32], [7001], 4, 4, 32, 64, "bf16")
+    check_attention([64, 70], [3000, 129], 2, 2, 64, 16, "bf16", causal=True)
+
+
+def test_attention_many_rows_sharp_and_flat():
+    for gain, sm in ((20.0, None), (0.0, None), (1.0, -0.3), (1.0, 0.0), (1e30, 1e-30), (1e-30, 1e29)):
+        check_attention([32, 32], [300, 90], 4, 4, 32, 64, "bf16", q_gain=gain, sm_scale=sm)
+
+
+def test_attention_many_rows_bad_pages_and_uneven_scales():
+    def bad(table, codes, scale, q):
+        table[0, 1], table[1, 0] = 10 ** 6, -1
+        scale[table[2, 1], :, 1] *= 2.0 ** 40
+        scale[table[2, 2], :, 1] = 0.0
+        codes[1, table[2, 2]] = 0
+        table[:, -1] = 2 ** 31 - 1
+    O, lse = check_attention([32, 32, 32], [150, 9, 190], 4, 4, 32, 16, "bf16", hook=bad,
+                             want_flags=lime_kv.LIME_FLAG_BAD_BLOCK)
+    assert (O[32:64] == 0).all() and torch.isneginf(lse[32:64]).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dh", [16, 32, 64, 128])
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
