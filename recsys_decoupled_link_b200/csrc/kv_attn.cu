@@ -109,6 +109,22 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The largest of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // The same onto zero.
 __device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, uint32_t b0,
                                                uint32_t b1) {
@@ -208,8 +224,10 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
   }
+  const int bs = 1 << a.log_block;
+  const int nb = bs >= TK ? 1 : TK / bs;   // blocks of a tile, each with an arrival of its own
   if (lane == 0)
-    for (int s = 0; s < S; ++s) mbar_init(&full[warp][s], 1);
+    for (int s = 0; s < S; ++s) mbar_init(&full[warp][s], nb);
   fence_mbar_init();
   __syncthreads();
   pdl_launch();
@@ -229,8 +247,6 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
   }
   __syncwarp();
 
-  const int bs = 1 << a.log_block;
-  const int nb = bs >= TK ? 1 : TK / bs;   // blocks of a tile
   const int box_rows = bs >= TK ? TK : bs;
   const uint32_t box_bytes = (uint32_t)box_rows * DH;
   const int batch = 32 / nb;               // tiles whose table entries a warp holds
@@ -297,31 +313,19 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     load_batch(batch, ent1, sc1);
     int base = 0;                        // first tile of batch 0
 
-    // tile j goes to ring stage `st`
+    // Tile j goes to ring stage `st`: the lane that holds a block's entry brings it.
     auto issue = [&](int j, uint32_t st) {
-      const int src = (j - base) * nb + lane % nb;
-      const int b0 = __shfl_sync(0xffffffffu, ent0, src & 31);
-      const int b1 = __shfl_sync(0xffffffffu, ent1, src & 31);
-      const int b = src < batch * nb ? b0 : b1;
-      const bool ok = lane < nb && b >= 0;
-      const unsigned live = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0)
-        mbar_arrive_expect_tx(&full[warp][st], (uint32_t)__popc(live) * box_bytes * 2);
-      __syncwarp();
-      if (ok) {
-        const int row = bs >= TK ? (((t0 + gw + j * NW) * TK) & (bs - 1)) * DH / 128 : 0;
-        uint8_t* dst = ring + st * 2 * Tile<DH>::kBytes + lane * box_bytes;
-        const int z = b * a.Hkv + h;
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-            "l"((uint64_t)&map_k), "r"(0), "r"(row), "r"(z), "r"(smem_u32(&full[warp][st]))
-            : "memory");
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst + Tile<DH>::kBytes)),
-            "l"((uint64_t)&map_v), "r"(0), "r"(row), "r"(z), "r"(smem_u32(&full[warp][st]))
-            : "memory");
+      const int src = (j - base) * nb, i = lane - (src & 31);
+      if (i >= 0 && i < nb) {
+        const int b = src < 32 ? ent0 : ent1;
+        mbar_arrive_expect_tx(&full[warp][st], b >= 0 ? 2 * box_bytes : 0);
+        if (b >= 0) {
+          const int row = bs >= TK ? (((t0 + gw + j * NW) * TK) & (bs - 1)) * DH / 128 : 0;
+          uint8_t* dst = ring + st * 2 * Tile<DH>::kBytes + i * box_bytes;
+          const int z = b * a.Hkv + h;
+          tma_load_3d(dst, &map_k, 0, row, z, &full[warp][st]);
+          tma_load_3d(dst + Tile<DH>::kBytes, &map_v, 0, row, z, &full[warp][st]);
+        }
       }
     };
 
@@ -375,12 +379,36 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       }
     }
 
+    // Probabilities carry their block's value scale over a unit, the largest
+    // scale so far: log2 of the ratio joins the exponent, and the sum takes it
+    // out again.  A lane holds both for its block of the batch.
+    float lr0, inv0;
+    auto new_unit = [&] {
+      const float most = fmaxf(vref, warp_max(sc0.y));
+      if (most > vref) {
+        const float keep = vref / most;
+        vref = most;
+        const uint64_t keep2 = pack2(keep, keep);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              unpack2(mul2(pack2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]), keep2), o[mt][i][2 * hf],
+                      o[mt][i][2 * hf + 1]);
+      }
+      unit_log2(sc0.y, vref, &lr0, &inv0);
+    };
+    new_unit();
+
     for (int j = 0; j < count; ++j) {
       if (j - base == batch) {           // batch 0 is used up
         base += batch;
         ent0 = ent1;
         sc0 = sc1;
         load_batch(base + batch, ent1, sc1);
+        new_unit();
       }
       const uint8_t *ks = ring + stage * 2 * Tile<DH>::kBytes, *vs = ks + Tile<DH>::kBytes;
       mbar_wait(&full[warp][stage], (phase >> stage) & 1u, a.status, &abort_flag);
@@ -393,37 +421,16 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         const uint32_t flip = ((sub * DH >> 7) & 7) << 4;  // of the step's first row (0 but for DH 16)
 
         // ---- the blocks' scales; hidden keys
-        float kg[NC], vg[NC];
+        float kg[NC], lr[NC], inv[NC];
         bool hidden = false;
-        float vmax = 0.0f;
 #pragma unroll
         for (int x = 0; x < NC; ++x) {
           const int src = (j - base) * nb + (nb > 1 ? (sub + x * 16) >> a.log_block : 0);
           kg[x] = __shfl_sync(0xffffffffu, sc0.x, src);
-          vg[x] = __shfl_sync(0xffffffffu, sc0.y, src);
+          lr[x] = __shfl_sync(0xffffffffu, lr0, src);
+          inv[x] = __shfl_sync(0xffffffffu, inv0, src);
           hidden |= kg[x] < 0.0f;
-          vmax = fmaxf(vmax, vg[x]);
         }
-        // the value unit grows with the scales seen (rarely after the first)
-        if (vmax > vref) {
-          const float keep = vref / vmax;
-          vref = vmax;
-          const uint64_t keep2 = pack2(keep, keep);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-                unpack2(mul2(pack2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]), keep2), o[mt][i][2 * hf],
-                        o[mt][i][2 * hf + 1]);
-        }
-        // probabilities carry their block's value scale over the unit: log2 of
-        // the ratio joins the exponent, at least -60 (what is smaller adds
-        // nothing); the sum takes it out again
-        float lr[NC], inv[NC];
-#pragma unroll
-        for (int x = 0; x < NC; ++x) unit_log2(vg[x], vref, &lr[x], &inv[x]);
 
         // ---- scores
         float s[MT][2 * NG][4];
@@ -479,9 +486,9 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
             float best = -INFINITY;
 #pragma unroll
             for (int x = 0; x < NG; ++x) {
-              const float v = fmaxf(fmaxf(s[mt][2 * x][2 * hf], s[mt][2 * x][2 * hf + 1]),
-                                    fmaxf(s[mt][2 * x + 1][2 * hf], s[mt][2 * x + 1][2 * hf + 1]));
-              best = ONE ? fmaxf(best, v) : fmaxf(best, v * fmaxf(c_row[mt][hf] * kg[ONE ? 0 : x], kTiny));
+              const float v = max3(s[mt][2 * x][2 * hf], s[mt][2 * x][2 * hf + 1], s[mt][2 * x + 1][2 * hf]);
+              if (ONE) best = max3(best, v, s[mt][2 * x + 1][2 * hf + 1]);
+              else best = fmaxf(best, fmaxf(v, s[mt][2 * x + 1][2 * hf + 1]) * fmaxf(c_row[mt][hf] * kg[ONE ? 0 : x], kTiny));
             }
             if (ONE) best *= fmaxf(c_row[mt][hf] * kg[0], kTiny);
             top[mt][hf] = best;
