@@ -29,8 +29,8 @@ constexpr int kWarps = 4;
 
 // How a worker of NW warps divides the work: a pair's fixed cost in its tiles,
 // and the fewest tiles worth a worker of their own.
-template <int NW> constexpr int kPairCost = 3 * NW;
-template <int NW> constexpr int kLeast = 7 * NW;
+template <int NW> constexpr int kPairCost = 5 * NW;
+template <int NW> constexpr int kLeast = kPairCost<NW> + 4 * NW;
 
 // Per head dim: keys of a warp's tile (one ring stage), keys of one softmax
 // step, stages of the ring.

@@ -140,17 +140,16 @@ def lime_kv_reserve(dims, lens, new_offsets, block_table, free_blocks, n_free, l
     if not (lens.dtype is _i32 and new_offsets.dtype is _i64 and block_table.dtype is _i32
             and free_blocks.dtype is _i32 and n_free.dtype is _i32 and lens_out.dtype is _i32
             and n_free_out.dtype is _i32 and slot_map.dtype is _i64
-            and lens.shape == (B,) and new_offsets.shape == (B + 1,)
-            and block_table.shape == (B, dims.max_blocks) and free_blocks.shape == (cap,)
-            and n_free.shape == (1,) and lens_out.shape == (B,) and n_free_out.shape == (1,)
-            and slot_map.shape == (n,)
+            and new_offsets.numel() == B + 1 and block_table.numel() == B * dims.max_blocks
+            and n_free.numel() == 1 and lens_out.numel() == B and n_free_out.numel() == 1
             and lens.get_device() == dev and new_offsets.get_device() == dev
             and block_table.get_device() == dev and free_blocks.get_device() == dev
             and n_free.get_device() == dev and lens_out.get_device() == dev
             and n_free_out.get_device() == dev and slot_map.get_device() == dev
             and lens.is_contiguous() and new_offsets.is_contiguous()
             and block_table.is_contiguous() and free_blocks.is_contiguous()
-            and lens_out.is_contiguous() and slot_map.is_contiguous() and ws.device == dev):
+            and lens_out.is_contiguous() and slot_map.is_contiguous() and ws.device == dev
+            and slot_map.dim() == 1 and free_blocks.dim() == 1):
         _refuse(dev, ws, ("lens", lens, _i32, (B,)), ("new_offsets", new_offsets, _i64, (B + 1,)),
                 ("block_table", block_table, _i32, (B, dims.max_blocks)),
                 ("free_blocks", free_blocks, _i32, (-1,)), ("n_free", n_free, _i32, (1,)),
@@ -208,8 +207,8 @@ def lime_kv_attention(dims, Q, q_offsets, block_table, lens, k_cache, v_cache, s
     shape = (n, dims.Hq, dims.dh)
     if not (Q.dtype is dt and O.dtype is dt and q_offsets.dtype is _i64
             and block_table.dtype is _i32 and lens.dtype is _i32 and Q.shape == shape
-            and O.shape == shape and q_offsets.shape == (B + 1,)
-            and block_table.shape == (B, dims.max_blocks) and lens.shape == (B,)
+            and O.shape == shape and q_offsets.numel() == B + 1
+            and block_table.numel() == B * dims.max_blocks
             and Q.get_device() == dev and O.get_device() == dev and q_offsets.get_device() == dev
             and block_table.get_device() == dev and lens.get_device() == dev
             and O.is_contiguous() and q_offsets.is_contiguous() and block_table.is_contiguous()
