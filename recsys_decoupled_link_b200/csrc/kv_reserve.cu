@@ -62,15 +62,15 @@ __device__ __forceinline__ bool served(int need, int64_t rank, int height) {
   return need == 0 || (need > 0 && rank + need <= height);
 }
 
-// The slot of row t of a request with n rows whose new rows begin at row a of
-// the packed ones, and the table entry of a block that it starts.  first: rank
-// of the request's first new block, or -1 where it is refused.
-__device__ __forceinline__ int64_t place(int64_t t, int64_t u, int64_t a, int n, int64_t first,
+// The slot of row t of a request with n rows whose new rows are [a, b) of the
+// packed ones, and the table entry of a block that it starts.  first: rank of
+// the request's first new block, or -1 where it is refused.
+__device__ __forceinline__ int64_t place(int64_t t, int64_t u, int64_t a, int64_t b, int n, int64_t first,
                                          int log_bs, int max_blocks, int64_t n_blocks,
                                          int32_t* table, const int32_t* free_blocks, int height,
                                          unsigned* status) {
   const int64_t bs = 1 << log_bs, pos = n + (t - a), col = pos >> log_bs;
-  if (first < 0 || pos < n || col >= max_blocks) return -1;
+  if (first < 0 || t < a || t >= b || col >= max_blocks) return -1;
   const int64_t held = (n + bs - 1) >> log_bs;
   int64_t block = -1;
   if (col < held) {
@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kScanThreads)
                     const int32_t* lens, const int64_t* off, int32_t* table,
                     const int32_t* free_blocks, int64_t cap, const int32_t* n_free,
                     int32_t* lens_out, int32_t* n_free_out, int64_t* slots, unsigned* status) {
-  __shared__ int32_t s_off[kFusedRequests], s_len[kFusedRequests], s_need[kFusedRequests],
-      s_first[kFusedRequests];
+  __shared__ int32_t s_off[kFusedRequests], s_end[kFusedRequests], s_len[kFusedRequests],
+      s_need[kFusedRequests], s_first[kFusedRequests];
   __shared__ int taken;
   if (threadIdx.x == 0) taken = 0;
   const int64_t most = (int64_t)max_blocks << log_bs;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kScanThreads)
     s_off[u] = (int32_t)a;
     s_len[u] = n;
     s_need[u] = blocks_needed(n, b - a, log_bs, max_blocks);
-    s_first[u] = (int32_t)(b - a);                 // the row count, until its rank is known
+    s_end[u] = (int32_t)b;
   }
   __syncthreads();
   const int per = (int)ceil_div(B, kScanThreads);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kScanThreads)
   int64_t all;
   int64_t rank = block_scan(sum, &all);
   for (int u = u0; u < u1; ++u) {
-    const int need = s_need[u], rows = s_first[u];
+    const int need = s_need[u], rows = s_end[u] - s_off[u];
     const bool ok = served(need, rank, height);
     s_first[u] = ok ? (int32_t)(rank < height ? rank : height) : -1;
     if (need > 0) rank += need;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kScanThreads)
       const int mid = (lo + hi) >> 1;
       if (s_off[mid] <= t) lo = mid; else hi = mid;
     }
-    slots[t] = place(t, lo, s_off[lo], s_len[lo], s_first[lo], log_bs, max_blocks, n_blocks, table,
+    slots[t] = place(t, lo, s_off[lo], s_end[lo], s_len[lo], s_first[lo], log_bs, max_blocks, n_blocks, table,
                      free_blocks, height, status);
   }
 }
@@ -203,7 +203,7 @@ __global__ void k_reserve_fill(int64_t B, int64_t total, int log_bs, int max_blo
   if (t >= total) return;
   const int64_t u = owner_of(off, B, t);
   const int n = kv_len(lens, u, (int64_t)max_blocks << log_bs, status);
-  slots[t] = place(t, u, off[u], n, first[u], log_bs, max_blocks, n_blocks, table, free_blocks,
+  slots[t] = place(t, u, off[u], off[u + 1], n, first[u], log_bs, max_blocks, n_blocks, table, free_blocks,
                    stack_height(n_free, cap, status), status);
 }
 

@@ -119,6 +119,19 @@ def test_reserve_bad_values_stay_in_bounds():
     assert got[3][0] == -1                                           # its block was id 99
 
 
+@pytest.mark.parametrize("B", [3, 2500])
+def test_reserve_rows_of_nobody_get_no_slot(B):
+    # offsets that end before the packed rows do: flagged, and those rows stay out of every block
+    dims = lime_kv.make_kv_dims(1, 1, 16, 16, 3 * B, 2, "bf16")
+    ws = lime_kv.KvWorkspace(dims, B, 0)
+    tab, out, nfo = i32(np.full((B, 2), -1)), i32(np.zeros(B)), i32([0])
+    slots = torch.full((B + 9,), -7, dtype=torch.int64, device="cuda")
+    lime_kv.lime_kv_reserve(dims, i32(np.zeros(B)), offsets([1] * B), tab, i32(np.arange(3 * B)), i32([3 * B]), out,
+                            nfo, slots, ws)
+    assert lime.lime_get_status(ws) == lime.LIME_FLAG_BAD_OFFSETS
+    assert (slots[B:] == -1).all() and (slots[:B] >= 0).all() and (tab[:, 1] == -1).all()
+
+
 @pytest.mark.parametrize("B", [1, 70, 3000])
 @pytest.mark.parametrize("how", ["all", "some"])
 def test_release_equals_the_oracle(B, how):
@@ -361,6 +374,31 @@ def test_attention_single_rows(dtype, dh, bs):
 def test_attention_links(dtype, dh, Hq, Hkv, l):
     lens = [70, 0, 1, 200, 64]
     check_attention([l] * len(lens), lens, Hq, Hkv, dh, 64, dtype, strided=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hq,Hkv,dh,q", [(700, 2, 2, 32, 1), (2100, 1, 1, 16, 1), (2500, 2, 1, 128, 1),
+                                           (2200, 1, 1, 32, 3), (600, 2, 2, 64, 2)])
+def test_attention_many_requests(B, Hq, Hkv, dh, q, dtype):
+    # a warp to a pair, and more requests than a thread block sums by itself
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 70, B)
+    counts = rng.integers(0, q + 1, B) if q > 1 else np.ones(B, dtype=int)
+    lens[5], lens[B - 1] = 900, 0
+    check_attention(counts, lens, Hq, Hkv, dh, 16, dtype, causal=q > 1)
+
+
+def test_attention_rows_behind_the_last_request_are_left():
+    rng = np.random.default_rng(3)
+    table, codes, scale = make_pool(rng, [40], 1, 32, 16)
+    dims = lime_kv.make_kv_dims(1, 1, 32, 16, codes.shape[1], table.shape[1], "bf16")
+    ws = lime_kv.KvWorkspace(dims, 1, 5)
+    q = torch.ones(5, 1, 32, dtype=torch.bfloat16, device="cuda")
+    O, lse = torch.full_like(q, 9.0), torch.full((5, 1), 9.0, device="cuda")
+    lime_kv.lime_kv_attention(dims, q, offsets([3]), i32(table), i32([40]), torch.tensor(codes[0], device="cuda"),
+                              torch.tensor(codes[1], device="cuda"), torch.tensor(scale, device="cuda"), O, lse, ws)
+    assert lime.lime_get_status(ws) == lime.LIME_FLAG_BAD_OFFSETS
+    assert (O[3:] == 9.0).all() and (lse[3:] == 9.0).all() and (O[:3] != 9.0).any()
 
 
 @pytest.mark.parametrize("bs", [16, 32, 64, 128])
