@@ -1,5 +1,6 @@
 // Block tables and slot maps of the paged history cache, built on the GPU from
-// the requests' lengths, and the release of blocks.
+// the requests' lengths, and the release of blocks.  Bound by latency: a scan
+// over the requests between two rounds of loads.
 #include "lime_fast.cuh"
 #include "lime_kv.cuh"
 #include "sm100.cuh"
@@ -13,9 +14,11 @@ namespace {
 constexpr int kScanThreads = 1024;
 
 
-// Exclusive sum of one value per thread over the block; *total gets the sum.
+// Exclusive sum of one value per thread over the block's THREADS; *total gets
+// the sum.
+template <int THREADS>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
-  __shared__ int64_t part[kScanThreads / 32];
+  __shared__ int64_t part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
 #pragma unroll
@@ -26,7 +29,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
   if (lane == 31) part[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int64_t p = part[lane];
+    int64_t p = lane < THREADS / 32 ? part[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, p, o);
@@ -35,7 +38,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
     part[lane] = p;
   }
   __syncthreads();
-  *total = part[kScanThreads / 32 - 1];
+  *total = part[31];
   const int64_t before = warp ? part[warp - 1] : 0;
   __syncthreads();
   return before + x - v;
@@ -87,71 +90,108 @@ __device__ __forceinline__ int64_t place(int64_t t, int64_t u, int64_t a, int64_
 
 // Up to kFusedRequests requests: one kernel.  Every thread block scans all of
 // them (12 bytes each, from L2) and places its own kFusedRows rows, so nothing
-// passes between blocks: 4.1 us for 256 requests with a row each, where two
-// kernels took 6.9.
+// passes between blocks.  A thread places ROWS rows in a row, with one search for
+// their request and mostly one block: 4 where there are rows enough to fill the
+// GPU (633,000 rows: 8.1 us against 11.7 with one), 1 where not (256 rows: 3.9
+// against 5.7 with four).
 constexpr int kFusedRequests = 2048;
-constexpr int kFusedRows = 2048;
+constexpr int kFusedThreads = 256;
 
-__global__ void __launch_bounds__(kScanThreads)
-    k_reserve_fused(int64_t B, int64_t total, int log_bs, int max_blocks, int64_t n_blocks,
+template <int ROWS>
+__global__ void __launch_bounds__(kFusedThreads)
+    k_reserve_fused(int B, int64_t total, int log_bs, int max_blocks, int64_t n_blocks,
                     const int32_t* lens, const int64_t* off, int32_t* table,
                     const int32_t* free_blocks, int64_t cap, const int32_t* n_free,
                     int32_t* lens_out, int32_t* n_free_out, int64_t* slots, unsigned* status) {
-  __shared__ int32_t s_off[kFusedRequests], s_end[kFusedRequests], s_len[kFusedRequests],
-      s_need[kFusedRequests], s_first[kFusedRequests];
+  extern __shared__ int32_t s_off[];
+  int32_t *s_end = s_off + B, *s_len = s_end + B, *s_need = s_len + B, *s_first = s_need + B;
   __shared__ int taken;
   if (threadIdx.x == 0) taken = 0;
   const int64_t most = (int64_t)max_blocks << log_bs;
   const int height = stack_height(n_free, cap, status);
-  for (int u = threadIdx.x; u < B; u += kScanThreads) {
+  for (int u = threadIdx.x; u < B; u += kFusedThreads) {
     int64_t a, b;
     user_range(off, u, B, total, &a, &b, status);
     const int n = kv_len(lens, u, most, status);
     s_off[u] = (int32_t)a;
+    s_end[u] = (int32_t)b;
     s_len[u] = n;
     s_need[u] = blocks_needed(n, b - a, log_bs, max_blocks);
-    s_end[u] = (int32_t)b;
   }
   __syncthreads();
-  const int per = (int)ceil_div(B, kScanThreads);
-  const int u0 = per * threadIdx.x, u1 = u0 + per < B ? u0 + per : (int)B;
+  const int per = (B + kFusedThreads - 1) / kFusedThreads;
+  const int u0 = per * threadIdx.x, u1 = u0 + per < B ? u0 + per : B;
   int64_t sum = 0;
   for (int u = u0; u < u1; ++u) sum += s_need[u] > 0 ? s_need[u] : 0;
   int64_t all;
-  int64_t rank = block_scan(sum, &all);
+  int64_t rank = block_scan<kFusedThreads>(sum, &all);
+  bool refused = false;
   for (int u = u0; u < u1; ++u) {
     const int need = s_need[u], rows = s_end[u] - s_off[u];
     const bool ok = served(need, rank, height);
     s_first[u] = ok ? (int32_t)(rank < height ? rank : height) : -1;
     if (need > 0) rank += need;
+    refused |= !ok;
     if (blockIdx.x == 0) {
       lens_out[u] = s_len[u] + (ok ? rows : 0);
-      if (!ok) raise_flag(status, LIME_FLAG_NO_BLOCKS);
       if (ok && need > 0) atomicMax(&taken, (int)rank);
     }
   }
-  __syncthreads();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *n_free_out = height - taken;
-  const int64_t t0 = (int64_t)blockIdx.x * kFusedRows;
-  for (int64_t t = t0 + threadIdx.x; t < t0 + kFusedRows && t < total; t += kScanThreads) {
-    int lo = 0, hi = (int)B;                       // the largest u with off[u] <= t is in [lo, hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_off[mid] <= t) lo = mid; else hi = mid;
+  refused = __syncthreads_or(refused);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *n_free_out = height - taken;
+    if (refused) raise_flag(status, LIME_FLAG_NO_BLOCKS);
+  }
+
+  const int64_t t0 = ((int64_t)blockIdx.x * kFusedThreads + threadIdx.x) * ROWS;
+  if (t0 >= total) return;
+  int u = 0;
+  for (int hi = B; hi - u > 1;) {                  // the largest u with off[u] <= t0 is in [u, hi)
+    const int mid = (u + hi) >> 1;
+    if (s_off[mid] <= t0) u = mid; else hi = mid;
+  }
+  int64_t out[ROWS], col = -1, base = -1;          // base: first slot of the block in column col
+  const int64_t mask = (1 << log_bs) - 1;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t t = t0 + i;
+    while (u + 1 < B && t >= s_off[u + 1]) ++u, col = -1;
+    const int64_t pos = s_len[u] + (t - s_off[u]);
+    if (col != pos >> log_bs || (pos & mask) == 0) {
+      const int64_t slot = t < total ? place(t, u, s_off[u], s_end[u], s_len[u], s_first[u], log_bs, max_blocks,
+                                             n_blocks, table, free_blocks, height, status)
+                                     : -1;
+      col = pos >> log_bs;
+      base = slot < 0 ? -1 : slot - (pos & mask);
     }
-    slots[t] = place(t, lo, s_off[lo], s_end[lo], s_len[lo], s_first[lo], log_bs, max_blocks, n_blocks, table,
-                     free_blocks, height, status);
+    out[i] = base < 0 || t >= s_end[u] ? -1 : base + (pos & mask);
+  }
+  if (ROWS % 2 == 0 && t0 + ROWS <= total && ((uintptr_t)slots & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i + 1 < ROWS; i += 2)
+      *reinterpret_cast<longlong2*>(slots + t0 + i) = make_longlong2(out[i], out[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (t0 + i < total) slots[t0 + i] = out[i];
   }
 }
 
-// More requests: a scan and a placing kernel.  A block of threads owns
-// kScanThreads requests and sums the needs of all before them itself.
-// first[u] becomes the rank of request u's first new block on the stack, or -1
-// where the request is refused.
+// More requests: a block of threads owns kScanThreads of them and sums the needs
+// of all before them itself.  With at most kShortRows rows to a request on
+// average (slots != NULL) it also places them, a thread or, beyond 32 rows, a
+// warp to a request; otherwise a second kernel does, by rows, which first[u]
+// tells the rank of request u's first new block on the stack, or -1 where the
+// request is refused.  65,000 rows of 16,384 requests: one kernel 12.0 us, two
+// 15.2.
+constexpr int kShortRows = 32;
+
 __global__ void __launch_bounds__(kScanThreads)
-    k_reserve_scan(int64_t B, int64_t total, int log_bs, int max_blocks, const int32_t* lens,
-                   const int64_t* off, int64_t cap, const int32_t* n_free, int32_t* lens_out,
-                   int32_t* n_free_out, int32_t* first, unsigned* status) {
+    k_reserve_scan(int64_t B, int64_t total, int log_bs, int max_blocks, int64_t n_blocks,
+                   const int32_t* lens, const int64_t* off, int32_t* table,
+                   const int32_t* free_blocks, int64_t cap, const int32_t* n_free,
+                   int32_t* lens_out, int32_t* n_free_out, int32_t* first, int64_t* slots,
+                   unsigned* status) {
   __shared__ int taken;
   pdl_launch();
   pdl_wait();
@@ -159,11 +199,14 @@ __global__ void __launch_bounds__(kScanThreads)
   const int height = stack_height(n_free, cap, status);
   const int64_t begin = (int64_t)blockIdx.x * kScanThreads, u = begin + threadIdx.x;
   int64_t sum = 0;
-#pragma unroll 4
+  // (their own blocks of threads flag what is wrong with them)
+#pragma unroll 8
   for (int64_t v = threadIdx.x; v < begin; v += kScanThreads) {
-    int64_t a, b;
-    user_range(off, v, B, total, &a, &b, status);
-    const int need = blocks_needed(kv_len(lens, v, most, status), b - a, log_bs, max_blocks);
+    int64_t x = off[v], y = off[v + 1], n = lens[v];
+    x = x < 0 ? 0 : x > total ? total : x;
+    y = y < x ? x : y > total ? total : y;
+    n = n < 0 ? 0 : n > most ? most : n;
+    const int need = blocks_needed((int)n, y - x, log_bs, max_blocks);
     sum += need > 0 ? need : 0;
   }
   int64_t a = 0, b = 0, before, all;
@@ -173,22 +216,52 @@ __global__ void __launch_bounds__(kScanThreads)
     n = kv_len(lens, u, most, status);
     need = blocks_needed(n, b - a, log_bs, max_blocks);
   }
-  block_scan(sum, &before);
-  const int64_t rank = before + block_scan(need > 0 ? need : 0, &all);
+  block_scan<kScanThreads>(sum, &before);
+  const int64_t rank = before + block_scan<kScanThreads>(need > 0 ? need : 0, &all);
   if (threadIdx.x == 0) taken = (int)(before < height ? before : height);
   __syncthreads();
+  int64_t mine = -1;                               // rank of this request's first block
+  bool refused = false;
   if (u < B) {
     const bool ok = served(need, rank, height);
-    first[u] = ok ? (int32_t)(rank < height ? rank : height) : -1;
+    if (!slots) first[u] = ok ? (int32_t)(rank < height ? rank : height) : -1;
     lens_out[u] = n + (ok ? (int)(b - a) : 0);
-    if (!ok) raise_flag(status, LIME_FLAG_NO_BLOCKS);
     if (ok && need > 0) atomicMax(&taken, (int)(rank + need));
+    refused = !ok;
+    mine = ok ? (rank < height ? rank : height) : -1;
   }
-  __syncthreads();
+  refused = __syncthreads_or(refused);
+  if (refused && threadIdx.x == 0) raise_flag(status, LIME_FLAG_NO_BLOCKS);
   // the block in which the stack runs out, or the last one, knows what is taken
   const bool last = begin + kScanThreads >= B;
   if (threadIdx.x == 0 && before <= height && (last || before + all > height))
     *n_free_out = height - taken;
+  if (!slots) return;
+  const bool few = b - a <= 32;
+  if (few) {
+    const int64_t mask = (1 << log_bs) - 1;
+    int64_t base = -1;                             // first slot of the current block
+    for (int64_t t = a; t < b; ++t) {
+      const int64_t pos = n + (t - a);
+      if (t == a || (pos & mask) == 0) {
+        const int64_t slot = place(t, u, a, b, n, mine, log_bs, max_blocks, n_blocks, table, free_blocks, height,
+                                   status);
+        base = slot < 0 ? -1 : slot - (pos & mask);
+      }
+      slots[t] = base < 0 ? -1 : base + (pos & mask);
+    }
+  }
+  for (unsigned left = __ballot_sync(0xffffffffu, !few); left; left &= left - 1) {
+    const int src = __ffs(left) - 1;
+    const int64_t wa = __shfl_sync(0xffffffffu, a, src), wb = __shfl_sync(0xffffffffu, b, src);
+    const int64_t wu = __shfl_sync(0xffffffffu, u, src), wm = __shfl_sync(0xffffffffu, mine, src);
+    const int wn = __shfl_sync(0xffffffffu, n, src);
+    for (int64_t t = wa + (threadIdx.x & 31); t < wb; t += 32)
+      slots[t] = place(t, wu, wa, wb, wn, wm, log_bs, max_blocks, n_blocks, table, free_blocks, height, status);
+  }
+  // rows that the offsets give to nobody
+  if (last && u == B - 1)
+    for (int64_t t = b; t < total; ++t) slots[t] = -1;
 }
 
 // One thread per new row: its slot, and the table entry of a block it starts.
@@ -226,7 +299,7 @@ __global__ void __launch_bounds__(kScanThreads)
     sum += ceil_div(n, bs) - ceil_div(kept_rows(keep, u, n), bs);
   }
   int64_t all;
-  int64_t at = height + block_scan(sum, &all);
+  int64_t at = height + block_scan<kScanThreads>(sum, &all);
   for (int64_t u = u0; u < u1; ++u) {
     const int n = kv_len(lens, u, most, status);
     const int k = kept_rows(keep, u, n);
@@ -264,18 +337,22 @@ int kv_reserve(const lime_kv_dims& D, int64_t B, const int32_t* lens, const int6
   int log_bs = 4;
   while (1 << log_bs < D.block) ++log_bs;
   if (B <= kFusedRequests) {
-    const int64_t grid = ceil_div(total, kFusedRows);
-    k_reserve_fused<<<(unsigned)(grid > 0 ? grid : 1), kScanThreads, 0, st>>>(
-        B, total, log_bs, D.max_blocks, D.n_blocks, lens, off, table, free_blocks, free_cap, n_free,
-        lens_out, n_free_out, slots, status);
+    const int rows = total >= (int64_t)num_sms() * 2 * kFusedThreads ? 4 : 1;
+    const int64_t grid = ceil_div(total, rows * kFusedThreads);
+    auto kernel = rows == 4 ? k_reserve_fused<4> : k_reserve_fused<1>;
+    kernel<<<(unsigned)(grid > 0 ? grid : 1), kFusedThreads, (size_t)B * 20, st>>>(
+        (int)B, total, log_bs, D.max_blocks, D.n_blocks, lens, off, table, free_blocks, free_cap,
+        n_free, lens_out, n_free_out, slots, status);
     note_launches(1);
     return LIME_OK;
   }
   int32_t* first = (int32_t*)ws;
+  const bool alone = total <= B * kShortRows;
   const int rc = launch_pdl(k_reserve_scan, dim3((unsigned)ceil_div(B, kScanThreads)),
-                            dim3(kScanThreads), 0, st, 1, B, total, log_bs, (int)D.max_blocks, lens,
-                            off, free_cap, n_free, lens_out, n_free_out, first, status);
-  if (rc || total == 0) return rc;
+                            dim3(kScanThreads), 0, st, 1, B, total, log_bs, (int)D.max_blocks,
+                            D.n_blocks, lens, off, table, free_blocks, free_cap, n_free, lens_out,
+                            n_free_out, first, alone ? slots : (int64_t*)nullptr, status);
+  if (rc || alone) return rc;
   return launch_pdl(k_reserve_fill, dim3((unsigned)ceil_div(total, 256)), dim3(256), 0, st, 1, B,
                     total, log_bs, (int)D.max_blocks, D.n_blocks, lens, off, table, free_blocks,
                     free_cap, n_free, (const int32_t*)first, slots, status);
