@@ -260,7 +260,9 @@ __global__ void __launch_bounds__(kScanThreads)
       slots[t] = place(t, wu, wa, wb, wn, wm, log_bs, max_blocks, n_blocks, table, free_blocks, height, status);
   }
   // rows that the offsets give to nobody
-  if (last && u == B - 1)
+  if (u == 0)
+    for (int64_t t = 0; t < a; ++t) slots[t] = -1;
+  if (u == B - 1)
     for (int64_t t = b; t < total; ++t) slots[t] = -1;
 }
 

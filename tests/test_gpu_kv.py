@@ -130,6 +130,30 @@ def test_reserve_rows_of_nobody_get_no_slot(B):
                             nfo, slots, ws)
     assert lime.lime_get_status(ws) == lime.LIME_FLAG_BAD_OFFSETS
     assert (slots[B:] == -1).all() and (slots[:B] >= 0).all() and (tab[:, 1] == -1).all()
+    # and offsets that begin behind row 0
+    late = offsets([1] * B) + 9
+    slots.fill_(-7)
+    lime_kv.lime_kv_reserve(dims, i32(np.zeros(B)), late, tab, i32(np.arange(3 * B)), i32([3 * B]), out, nfo, slots, ws)
+    assert lime.lime_get_status(ws) == lime.LIME_FLAG_BAD_OFFSETS
+    assert (slots[:9] == -1).all() and (slots[9:] >= 0).all()
+
+
+def test_calls_without_requests():
+    dims = lime_kv.make_kv_dims(2, 2, 16, 16, 8, 2, "bf16")
+    ws = lime_kv.KvWorkspace(dims, 0, 4)
+    none, n_free, out = torch.zeros(0, dtype=torch.int32, device="cuda"), i32([5]), i32([0])
+    off = torch.zeros(1, dtype=torch.int64, device="cuda")
+    table = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    lime_kv.lime_kv_reserve(dims, none, off, table, i32(np.arange(8)), n_free, none.clone(), out,
+                            torch.zeros(0, dtype=torch.int64, device="cuda"), ws)
+    assert int(out) == 5
+    lime_kv.lime_kv_release(dims, none, None, table, i32(np.arange(8)), n_free, none.clone(), out, ws)
+    assert int(out) == 5
+    k = torch.zeros(8, 2, 16, 16, dtype=torch.int8, device="cuda")
+    x, scale = torch.zeros(0, 2, 16, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 2, 2, device="cuda")
+    lime_kv.lime_kv_append(dims, x, x, torch.zeros(0, dtype=torch.int64, device="cuda"), k, k.clone(), scale, ws)
+    lime_kv.lime_kv_attention(dims, x, off, table, none, k, k.clone(), scale, x.clone(), None, ws)
+    assert lime.lime_get_status(ws) == 0
 
 
 @pytest.mark.parametrize("B", [1, 70, 3000])
@@ -688,3 +712,47 @@ def test_calls_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(O, second)
     assert c.status() == 0
+
+
+_CAPTURE_FIRST = r"""
+import torch
+from recsys_decoupled_link_b200 import lime_kv
+
+dims = lime_kv.make_kv_dims(4, 2, 32, 16, 40, 12, "bf16")
+c = lime_kv.HistoryCache(dims, 3, max_q=96)
+g = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn(60, 2, 2, 32, device="cuda", generator=g).to(torch.bfloat16)
+q = torch.randn(96, 4, 32, device="cuda", generator=g).to(torch.bfloat16)
+off = torch.tensor([0, 20, 59, 60], device="cuda")
+qoff = torch.tensor([0, 32, 64, 96], device="cuda")
+slots, O = torch.empty(60, dtype=torch.int64, device="cuda"), torch.empty_like(q)
+
+def calls():
+    lime_kv.lime_kv_reserve(dims, c.lens, off, c.table, c.free, c.n_free, c._lens, c._n_free, slots, c.ws)
+    lime_kv.lime_kv_append(dims, x[:, 0], x[:, 1], slots, c.k, c.v, c.scale, c.ws)
+    lime_kv.lime_kv_attention(dims, q, qoff, c.table, c._lens, c.k, c.v, c.scale, O, None, c.ws)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+first = O.clone()
+O.zero_()
+calls()
+assert c.status() == 0 and torch.equal(O, first) and bool((O != 0).any())
+print("capture-first ok")
+"""
+
+
+def test_calls_captured_before_any_eager_call():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, PYTHONPATH=root + os.pathsep + os.environ.get("PYTHONPATH", ""),
+               CUDA_MODULE_LOADING="EAGER")
+    r = subprocess.run([sys.executable, "-c", _CAPTURE_FIRST], cwd=root, env=env, capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0 and "capture-first ok" in r.stdout, r.stdout + r.stderr

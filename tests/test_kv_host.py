@@ -59,6 +59,12 @@ def test_workspace_bytes(kv):
 WS = 0x10000000
 
 
+def test_workspace_init_refuses(kv):
+    f = kv._lib.lime_kv_workspace_init
+    for args in ((None, 1 << 20), (WS + 64, 1 << 20), (WS, 64)):
+        assert f(*args, None) == kv_err(kv, "ARG"), args
+
+
 def _call(kv, fn, dims, names, base, **change):
     a = dict(base)
     a.update(change)
