@@ -77,12 +77,18 @@ class KvWorkspace:
 _i8, _i32, _i64, _f32 = torch.int8, torch.int32, torch.int64, torch.float32
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _device() -> int:
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    try:
+        return _current_device()
+    except RuntimeError:        # no GPU: every tensor is refused
+        return 0
 
 
 def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _refuse(dev: int, ws, *tensors):
@@ -156,7 +162,7 @@ def lime_kv_reserve(dims, lens, new_offsets, block_table, free_blocks, n_free, l
                 ("lens_out", lens_out, _i32, (B,)), ("n_free_out", n_free_out, _i32, (1,)),
                 ("slot_map", slot_map, _i64, (-1,)))
     rc = _lib.lime_kv_reserve(
-        ctypes.byref(dims), B, lens.data_ptr(), new_offsets.data_ptr(), n, block_table.data_ptr(),
+        dims, B, lens.data_ptr(), new_offsets.data_ptr(), n, block_table.data_ptr(),
         free_blocks.data_ptr(), cap, n_free.data_ptr(), lens_out.data_ptr(),
         n_free_out.data_ptr(), slot_map.data_ptr(), ws.address, ws.nbytes, _raw_stream(stream, dev))
     if rc:
@@ -171,7 +177,7 @@ def lime_kv_release(dims, lens, keep: Optional[torch.Tensor], block_table, free_
             ("free_blocks", free_blocks, _i32, (-1,)), ("n_free", n_free, _i32, (1,)),
             ("lens_out", lens_out, _i32, (B,)), ("n_free_out", n_free_out, _i32, (1,)))
     rc = _lib.lime_kv_release(
-        ctypes.byref(dims), B, lens.data_ptr(), None if keep is None else keep.data_ptr(),
+        dims, B, lens.data_ptr(), None if keep is None else keep.data_ptr(),
         block_table.data_ptr(), free_blocks.data_ptr(), free_blocks.shape[0], n_free.data_ptr(),
         lens_out.data_ptr(), n_free_out.data_ptr(), ws.address, ws.nbytes,
         _raw_stream(stream, dev))
@@ -192,7 +198,7 @@ def lime_kv_append(dims, K, V, slot_map, k_cache, v_cache, scale, ws: KvWorkspac
     ldk, ldv = _pitch("K", K, shape[1], shape[2]), _pitch("V", V, shape[1], shape[2])
     _check_pool(dims, dev, k_cache, v_cache, scale)
     rc = _lib.lime_kv_append(
-        ctypes.byref(dims), K.data_ptr(), ldk, V.data_ptr(), ldv, n, slot_map.data_ptr(),
+        dims, K.data_ptr(), ldk, V.data_ptr(), ldv, n, slot_map.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), scale.data_ptr(), ws.address, ws.nbytes,
         _raw_stream(stream, dev))
     if rc:
@@ -222,7 +228,7 @@ def lime_kv_attention(dims, Q, q_offsets, block_table, lens, k_cache, v_cache, s
     ldq = _pitch("Q", Q, shape[1], shape[2])
     _check_pool(dims, dev, k_cache, v_cache, scale)
     rc = _lib.lime_kv_attention(
-        ctypes.byref(dims), B, Q.data_ptr(), ldq, q_offsets.data_ptr(), n, block_table.data_ptr(),
+        dims, B, Q.data_ptr(), ldq, q_offsets.data_ptr(), n, block_table.data_ptr(),
         lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), scale.data_ptr(),
         1.0 / math.sqrt(dims.dh) if sm_scale is None else sm_scale, 1 if causal else 0,
         O.data_ptr(), None if lse is None else lse.data_ptr(), ws.address, ws.nbytes,
