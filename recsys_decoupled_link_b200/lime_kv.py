@@ -75,8 +75,6 @@ class KvWorkspace:
 
 
 _i8, _i32, _i64, _f32 = torch.int8, torch.int32, torch.int64, torch.float32
-
-
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -93,8 +91,9 @@ def _raw_stream(stream, dev: int) -> int:
 
 def _refuse(dev: int, ws, *tensors):
     """Raises for the first tensor (name, tensor, dtype, shape with -1 for any size, "strided"
-    where its rows may be) that is not what a call takes, or for a workspace elsewhere.  The calls test all of them in one expression first, and come here only to
-    name the one at fault: a call's checks are much of what a small call costs on the host."""
+    where its rows may be) that is not what a call takes, or for a workspace elsewhere.  The
+    calls test all of them in one expression first, and come here only to name the one at
+    fault: a call's checks are much of what a small call costs on the host."""
     for name, t, dtype, shape, *strided in tensors:
         if t is None:
             continue
@@ -271,16 +270,19 @@ class HistoryCache:
         slots = torch.empty(K.shape[0], dtype=torch.int64, device=K.device)
         lime_kv_reserve(self.dims, self.lens, new_offsets, self.table, self.free, self.n_free,
                         self._lens, self._n_free, slots, self.ws)
-        self._advance()
         lime_kv_append(self.dims, K, V, slots, self.k, self.v, self.scale, self.ws)
+        self._advance()             # a refused call leaves the lengths and the stack as they were
         return slots
 
     def attend(self, Q: torch.Tensor, q_offsets: torch.Tensor, causal: bool = False,
                sm_scale: Optional[float] = None, lse: Optional[torch.Tensor] = None):
         """Attention of Q [n, Hq, dh] over the cached rows; returns O [n, Hq, dh]."""
         if Q.shape[0] > self.max_q:
-            self.ws = KvWorkspace(self.dims, self.B, Q.shape[0], device=Q.device)
-            self.max_q = Q.shape[0]
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("Q: more rows than max_q; a capture needs the workspace beforehand")
+            ws = KvWorkspace(self.dims, self.B, Q.shape[0], device=self.k.device)
+            ws.buf[:4].copy_(self.ws.buf[:4])       # flags that status() has not read yet
+            self.ws, self.max_q = ws, Q.shape[0]
         O = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
         lime_kv_attention(self.dims, Q, q_offsets, self.table, self.lens, self.k, self.v,
                           self.scale, O, lse, self.ws, sm_scale, causal)

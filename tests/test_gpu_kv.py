@@ -672,6 +672,42 @@ def test_cache_serves_a_growing_history():
     attend([4, 4, 4, 4, 4], False)
 
 
+def test_cache_refused_rows_change_nothing():
+    dims = lime_kv.make_kv_dims(2, 2, 32, 16, 20, 4, "bf16")
+    cache, other = lime_kv.HistoryCache(dims, 2), lime_kv.HistoryCache(dims, 2)
+    x = torch.randn(50, 2, 2, 32, device="cuda").to(torch.bfloat16)
+    for bad in (x[:, 1].float(), x[:49, 1], x.transpose(0, 1)[1].transpose(1, 2).contiguous().transpose(1, 2)):
+        with pytest.raises(ValueError):
+            cache.append(x[:, 0], bad, offsets([20, 30]))
+    with pytest.raises(lime.LimeError):                              # row pitch of 65 elements
+        cache.append(x[:, 0], torch.zeros(50 * 65, dtype=torch.bfloat16, device="cuda").as_strided(
+            (50, 2, 32), (65, 32, 1)), offsets([20, 30]))
+    assert cache.lens.tolist() == [0, 0] and int(cache.n_free) == 20
+    for c in (cache, other):
+        c.append(x[:, 0], x[:, 1], offsets([20, 30]))
+    assert cache.lens.tolist() == [20, 30] and cache.status() == 0
+    q = torch.randn(8, 2, 32, device="cuda").to(torch.bfloat16)
+    assert torch.equal(cache.attend(q, offsets([4, 4])), other.attend(q, offsets([4, 4])))
+
+
+def test_cache_keeps_its_flags_when_its_workspace_grows():
+    dims = lime_kv.make_kv_dims(2, 2, 32, 16, 2, 4, "bf16")
+    cache = lime_kv.HistoryCache(dims, 2)
+    x = torch.randn(50, 2, 2, 32, device="cuda").to(torch.bfloat16)
+    cache.append(x[:, 0], x[:, 1], offsets([20, 30]))                # two blocks: the second request is refused
+    q = torch.randn(8, 2, 32, device="cuda").to(torch.bfloat16)
+    O = cache.attend(q, offsets([4, 4]))
+    assert cache.status() == lime_kv.LIME_FLAG_NO_BLOCKS and cache.status() == 0
+    assert cache.lens.tolist() == [20, 0] and (O[4:] == 0).all() and (O[:4] != 0).any()
+    graph = torch.cuda.CUDAGraph()
+    more = torch.randn(80, 2, 32, device="cuda").to(torch.bfloat16)
+    off = offsets([40, 40])
+    with pytest.raises(ValueError, match="max_q"):                   # its workspace would belong to the graph
+        with torch.cuda.graph(graph):
+            cache.attend(more, off)
+    assert torch.equal(cache.attend(more, off)[:1], cache.attend(more, off)[:1])
+
+
 def test_calls_on_another_stream_and_in_a_graph():
     rng = np.random.default_rng(13)
     B, Hq, Hkv, dh, bs = 3, 4, 2, 64, 16
