@@ -13,7 +13,6 @@ namespace {
 
 constexpr int kScanThreads = 1024;
 
-
 // Exclusive sum of one value per thread over the block's THREADS; *total gets
 // the sum.
 template <int THREADS>
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(kFusedThreads)
       const int64_t slot = t < total ? place(t, u, s_off[u], s_end[u], s_len[u], s_first[u], log_bs, max_blocks,
                                              n_blocks, table, free_blocks, height, status)
                                      : -1;
-      col = pos >> log_bs;
+      col = slot < 0 ? -1 : pos >> log_bs;         // the next row may be placed in the same block
       base = slot < 0 ? -1 : slot - (pos & mask);
     }
     out[i] = base < 0 || t >= s_end[u] ? -1 : base + (pos & mask);

@@ -138,6 +138,26 @@ def test_reserve_rows_of_nobody_get_no_slot(B):
     assert (slots[:9] == -1).all() and (slots[9:] >= 0).all()
 
 
+def test_reserve_many_rows_behind_rows_of_nobody():
+    # 80,000 rows: the first request begins at row 3, inside the rows that one thread places, and holds 5 rows
+    B, n, bs = 3, 80_000, 128
+    dims = lime_kv.make_kv_dims(1, 1, 16, bs, 700, 300, "bf16")
+    ws = lime_kv.KvWorkspace(dims, B, 0)
+    counts, lens = np.array([26_667, 26_665, 26_665]), np.array([5, 6, 128])
+    table = np.full((B, 300), -1)
+    table[:, 0] = [690, 691, 692]
+    tab, out, nfo = i32(table), i32(np.zeros(B)), i32([0])
+    slots = torch.full((n,), -7, dtype=torch.int64, device="cuda")
+    lime_kv.lime_kv_reserve(dims, i32(lens), offsets(counts) + 3, tab, i32(np.arange(690)), i32([690]), out, nfo,
+                            slots, ws)
+    assert lime.lime_get_status(ws) == lime.LIME_FLAG_BAD_OFFSETS
+    lens_w, nf_w, tab_w, slots_w, _ = K.reserve(lens, counts, table, np.arange(690), 690, bs)
+    np.testing.assert_array_equal(slots.cpu()[3:], slots_w)
+    assert (slots[:3] == -1).all() and int(nfo) == nf_w
+    np.testing.assert_array_equal(tab.cpu(), tab_w)
+    np.testing.assert_array_equal(out.cpu(), lens_w)
+
+
 def test_calls_without_requests():
     dims = lime_kv.make_kv_dims(2, 2, 16, 16, 8, 2, "bf16")
     ws = lime_kv.KvWorkspace(dims, 0, 4)
