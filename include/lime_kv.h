@@ -141,8 +141,10 @@ int lime_kv_append(const lime_kv_dims* dims, const void* K, int64_t ldk, const v
  * no row gets a zero output and lse = -inf.  Scores, sums and outputs are fp32.
  * Queries enter the score product exactly (bf16) or as two fp16 terms (fp32);
  * probabilities enter the value product as one fp16 term (bf16 dtype) or two
- * (fp32), relative to the row's largest, to 2^-39 of which they are exact: what
- * a row's tail below that weighs is lost.  Codes behind a request's last row
+ * (fp32), each times its block's value scale over the largest such scale among
+ * the request's blocks, to 2^-39 of the row's largest probability: what weighs
+ * less is lost, so an output is off by up to 2^-39 of the request's largest
+ * value for each row.  Codes behind a request's last row
  * are never used.  A table entry outside the pool hides its rows and sets
  * LIME_FLAG_BAD_BLOCK. */
 int lime_kv_attention(const lime_kv_dims* dims, int64_t B, const void* Q, int64_t ldq,

@@ -56,7 +56,6 @@ template <int DH> struct Tile {
   static constexpr int kRing = kStages * 2 * kBytes; // per warp
 };
 
-
 // ------------------------------------------------------------------- plan
 
 // Prefix sums of the requests' weights, where there are too many requests for
@@ -687,7 +686,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
       if (before_me == last - first) {
         if (gt == 0) a.tickets[first] = 0;
         __threadfence();
-        join_parts<R, DH>(a, first, last, gt, NW * 32, out_rows, [](int) { return true; }, store);
+        join_parts<R, DH>(a, first, last, gt, NW * 32, out_rows, store);
       }
     }
     fence_proxy_async_smem();            // the ring's next writes are TMA's

@@ -1,6 +1,6 @@
-// What the two kernels of the cache attention share (kv_attn.cu, kv_attn_tc.cu):
-// the division of ragged requests over persistent workers, the joining of cut
-// pairs, and the arithmetic of codes and probabilities.
+// Parts of the cache attention (kv_attn.cu): the division of ragged requests over
+// persistent workers, the joining of cut pairs, and the arithmetic of codes and
+// probabilities.
 #pragma once
 #include <cuda_fp16.h>
 #include <math.h>
@@ -64,7 +64,7 @@ __device__ __forceinline__ int64_t div_by(int64_t x, int64_t y) {
 
 // How requests are cut into pairs, and pairs into tiles.
 struct Cut {
-  int heads;  // kv heads, or groups of them, of a request
+  int heads;  // kv heads of a request
   int R;      // rows of a pair
   int TK;     // keys of a tile
   int cost;   // a pair's fixed cost, in tiles
@@ -196,7 +196,7 @@ struct Segment {
 // The segment at sg.pos, found from the request of the one before it (every
 // lane of a warp calls it; sg is the warp's own copy).
 struct Head {
-  int h, rt;   // kv head (or group), tile of rows
+  int h, rt;   // kv head, tile of rows
   int t0, t1;  // tiles of the pair
 };
 __device__ __forceinline__ Head next_segment(const Args& a, const Cut& cut, volatile Segment& sg) {
@@ -273,13 +273,12 @@ __device__ __forceinline__ float* part_of(const Args& a, int c, int first) {
 }
 
 // Joins the parts of workers first..last in their order; threads 0..threads-1
-// each take outputs (row, 4 dims) of rows for which valid(row).
-template <int R, int DH, typename Valid, typename Store>
+// each take outputs (row, 4 dims).
+template <int R, int DH, typename Store>
 __device__ __forceinline__ void join_parts(const Args& a, int first, int last, int thread,
-                                           int threads, int rows, Valid valid, Store store) {
+                                           int threads, int rows, Store store) {
   for (int i = thread; i < rows * (DH / 4); i += threads) {
     const int r = i / (DH / 4), d = i % (DH / 4) * 4;
-    if (!valid(r)) continue;
     float top = -INFINITY, sum = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int c0 = first; c0 <= last; c0 += kJoin) {
