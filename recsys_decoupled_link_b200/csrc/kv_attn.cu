@@ -277,11 +277,12 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     const int t_live = (lim_high + TK - 1) / TK;
     const int t1 = head.t1 < t_live ? head.t1 : t_live;
 
-    float o[MT][NT][4], m[MT][2], vref = 0.0f;
+    // from: kOffset less the row's reference; a probability's exponent adds it
+    float o[MT][NT][4], from[MT][2], vref = 0.0f;
     uint64_t l[MT][2];                   // sums of the even and the odd columns
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = -INFINITY;
+      from[mt][0] = from[mt][1] = kUnseen;
       l[mt][0] = l[mt][1] = 0;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -335,9 +336,8 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         if (b >= 0) {
           const int row = bs >= TK ? (((t0 + gw + j * NW) * TK) & (bs - 1)) * DH / 128 : 0;
           uint8_t* dst = ring + st * 2 * Tile<DH>::kBytes + i * box_bytes;
-          const int z = b * a.Hkv + h;
-          tma_load_3d(dst, &map_k, 0, row, z, &full[warp][st]);
-          tma_load_3d(dst + Tile<DH>::kBytes, &map_v, 0, row, z, &full[warp][st]);
+          tma_load_3d(dst, &map_k, 0, row, b, &full[warp][st]);
+          tma_load_3d(dst + Tile<DH>::kBytes, &map_v, 0, row, b, &full[warp][st]);
         }
       }
     };
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
     new_unit();
 
     for (int j = 0; j < count; ++j) {
-      if (j - base == batch) {           // batch 0 is used up
+      if (__builtin_expect(j - base == batch, 0)) {  // batch 0 is used up
         base += batch;
         ent0 = ent1;
         sc0 = sc1;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
 #pragma unroll 1
       for (int sub = 0; sub < TK; sub += SK) {
         const int key0 = (t0 + gw + j * NW) * TK + sub;
-        if (key0 >= lim_high) break;
+        if (sub > 0 && key0 >= lim_high) break;
         const uint32_t flip = ((sub * DH >> 7) & 7) << 4;  // of the step's first row (0 but for DH 16)
 
         // ---- the blocks' scales; hidden keys
@@ -444,6 +444,13 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
           inv[x] = __shfl_sync(0xffffffffu, inv0, src);
           hidden |= kg[x] < 0.0f;
         }
+        float c[MT][2][NC];                  // factors of a score to units of log2
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int x = 0; x < NC; ++x) c[mt][hf][x] = c_row[mt][hf] * kg[x];
 
         // ---- scores
         float s[MT][2 * NG][4];
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
           }
         }
 
-        if (hidden || key0 + SK > lim_low) {
+        if (__builtin_expect(hidden || key0 + SK > lim_low, 0)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -485,8 +492,11 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
             }
           }
 #pragma unroll
-          for (int x = 0; x < NC; ++x)
-            if (kg[x] < 0.0f) kg[x] = 1.0f;  // the marker is no factor
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int x = 0; x < NC; ++x) c[mt][hf][x] = fmaxf(c[mt][hf][x], kTiny);  // -inf times 0 is NaN
         }
 
         // ---- running maximum, in units of log2
@@ -501,29 +511,28 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
             for (int x = 0; x < NG; ++x) {
               const float v = max3(s[mt][2 * x][2 * hf], s[mt][2 * x][2 * hf + 1], s[mt][2 * x + 1][2 * hf]);
               if (ONE) best = max3(best, v, s[mt][2 * x + 1][2 * hf + 1]);
-              else best = fmaxf(best, fmaxf(v, s[mt][2 * x + 1][2 * hf + 1]) * fmaxf(c_row[mt][hf] * kg[ONE ? 0 : x], kTiny));
+              else best = fmaxf(best, fmaxf(v, s[mt][2 * x + 1][2 * hf + 1]) * c[mt][hf][ONE ? 0 : x]);
             }
-            if (ONE) best *= fmaxf(c_row[mt][hf] * kg[0], kTiny);
             top[mt][hf] = best;
-            grow |= best > m[mt][hf] + kSlack;
+            grow |= (ONE ? fmaf(best, c[mt][hf][0], from[mt][hf]) : best + from[mt][hf]) > kOffset + kSlack;
           }
         }
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               float v = top[mt][hf];
+              if (ONE) v *= c[mt][hf][0];
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-              v = fmaxf(v, m[mt][hf]);
-              const float keep = ex2(m[mt][hf] - (v == -INFINITY ? 0.0f : v));
-              m[mt][hf] = v;
-              l[mt][hf] = mul2(l[mt][hf], pack2(keep, keep));
-              const uint64_t ok = pack2(keep, keep);
+              const float to = fminf(from[mt][hf], kOffset - v), keep = ex2(to - from[mt][hf]);
+              from[mt][hf] = to;
+              const uint64_t keep2 = pack2(keep, keep);
+              l[mt][hf] = mul2(l[mt][hf], keep2);
 #pragma unroll
               for (int i = 0; i < NT; ++i)
-                unpack2(mul2(pack2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]), ok), o[mt][i][2 * hf],
+                unpack2(mul2(pack2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]), keep2), o[mt][i][2 * hf],
                        o[mt][i][2 * hf + 1]);
             }
           }
@@ -535,16 +544,14 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const float from = kOffset - (m[mt][hf] == -INFINITY ? 0.0f : m[mt][hf]);
 #pragma unroll
             for (int x = 0; x < NG; ++x) {
-              const float c = fmaxf(c_row[mt][hf] * kg[ONE ? 0 : x], kTiny);
-              const float add = from + lr[ONE ? 0 : x];
+              const float by_c = c[mt][hf][ONE ? 0 : x], add = from[mt][hf] + lr[ONE ? 0 : x];
               float p[4];
 #pragma unroll
               for (int i = 0; i < 4; i += 2) {
                 unpack2(fma2(pack2(s[mt][2 * x + (i >> 1)][2 * hf], s[mt][2 * x + (i >> 1)][2 * hf + 1]),
-                            pack2(c, c), pack2(add, add)),
+                            pack2(by_c, by_c), pack2(add, add)),
                        p[i], p[i + 1]);
                 p[i] = ex2(p[i]);
                 p[i + 1] = ex2(p[i + 1]);
@@ -613,7 +620,7 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int r = mt * 16 + hf * 8 + g;
-        if (t == 0) ml[warp][r] = make_float2(m[mt][hf], sum);
+        if (t == 0) ml[warp][r] = make_float2(from[mt][hf] == kUnseen ? -INFINITY : -from[mt][hf], sum);
         // NaN sums stay NaN; a row that saw no key gives 0
         const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
         float out[E];

@@ -19,7 +19,8 @@ constexpr int kInlineRequests = 2048;    // most requests whose weights every bl
 constexpr int kJoin = 8;                 // parts of a cut pair read at a time
 constexpr float kOffset = 14.0f;         // probabilities enter fp16 times 2^14
 constexpr float kSlack = 1.5f;           // log2 by which a row's reference may lag its maximum
-constexpr float kTiny = 1e-37f;          // least factor of a score: -inf times 0 would be NaN
+constexpr float kTiny = 1e-37f;          // least factor of a masked score
+constexpr float kUnseen = 3.0e38f;       // kOffset less the reference of a row that has seen no key
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -250,15 +251,16 @@ __device__ __forceinline__ int limit_of(const Args& a, volatile Segment& sg, int
 }
 
 // One (key, value) scale entry of the table: block `col` of the segment's
-// request, for kv head h.  A negative key scale hides the block.
+// request, for kv head h, and the pair's place among the (block, head)s.  A
+// negative key scale hides the block.
 __device__ __forceinline__ void load_entry(const Args& a, volatile Segment& sg, int h, int col,
-                                           int* block, float2* sc) {
-  *block = -1;
+                                           int* place, float2* sc) {
+  *place = -1;
   *sc = make_float2(-1.0f, 0.0f);
   if (col >= (sg.n + (1 << a.log_block) - 1) >> a.log_block) return;
   const int b = a.table[sg.u * a.max_blocks + col];
   if (b >= 0 && b < a.n_blocks) {
-    *block = b;
+    *place = b * a.Hkv + h;
     *sc = a.scale[(int64_t)b * a.Hkv + h];
   } else {
     raise_flag(a.status, LIME_FLAG_BAD_BLOCK);
@@ -323,7 +325,7 @@ __device__ __forceinline__ void store_out(const Args& a, int64_t at, int d, floa
     *reinterpret_cast<float4*>(dst) = v;
   else
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - kOffset) * kLn2;
+  if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // Powers of two that bring a row whose largest magnitude is top (finite, or
