@@ -16,20 +16,22 @@
 // operands from shared memory or TMEM, which adds a store and a load of two
 // bytes for every code read once (and block-diagonal queries where a head has
 // fewer than 128 rows); built that way, with the probabilities in TMEM, the
-// kernel took 76 us where this one takes 56 (32 links over 16,384 rows), 71
-// against 55 (causal chunks) and 133 against 134 (64 links, ragged).  mma.sync
+// kernel took 76 us where this one takes 54 (32 links over 16,384 rows), 71
+// against 55 (causal chunks) and 133 against 128 (64 links, ragged).  mma.sync
 // reaches 552 TFLOP/s here, which is never the bound.  Which key a fragment's
 // column stands for, and which dims a lane holds, are free as long as both
 // products agree; KeyMap picks them so that every shared-memory read is a wide
 // one without bank conflicts.
 //
 // Measured (B200, graph replay): 64 requests' single tokens, 32 query heads on 8,
-// dh 128, 508,000 rows in all: 179 us, 5.8 TB/s, 89 % of the copy bandwidth.
-// 32 x 32 links over 16,384 rows, 4 heads of 32: 56 us, 2.4 TB/s; there a warp
-// holds 32 rows, two blocks of four warps fill an SM's registers, and the
-// chains between score product, exponentials and value product bound it (issue
-// 41 %, tensor 29 %, special-function pipe 30 %).  Three blocks spill (58 us),
-// row tiles of 16 or 64 took 74 and 58.
+// dh 128, 508,000 rows in all: 174 us, 6.0 TB/s, 91 % of the copy bandwidth.
+// 32 x 32 links over 16,384 rows, 4 heads of 32: 54 us, 2.5 TB/s; there a warp
+// holds 32 rows and two blocks of four warps fill an SM's registers.  A tile of
+// 64 keys takes a warp about 700 instructions, 64 of them mma.sync at four to
+// five issue slots each: 1,000 of the 1,800 cycles that a scheduler spends on it
+// (tensor and special-function pipe: 500 each).  Three blocks spill (58 us) or,
+// with steps of 32 keys, spend more on their steps (62 us); row tiles of 16 took
+// 74 us, of 64 (64 links, ragged) 159 against 134.
 #include "kv_attn.cuh"
 
 namespace lime {
