@@ -57,7 +57,8 @@ typedef struct {
 
 /* Bytes of device workspace for calls with up to B requests and total_q query
  * rows (256-byte aligned, prepared once by lime_kv_workspace_init); 0 for
- * unsupported dims. */
+ * unsupported dims.  The same for every total_q > 0: a workspace made for one
+ * query row serves any number of them. */
 size_t lime_kv_workspace_bytes(const lime_kv_dims* dims, int64_t B, int64_t total_q);
 
 /* Clears the workspace's status word and the counters that the calls leave at

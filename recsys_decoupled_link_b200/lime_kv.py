@@ -245,7 +245,8 @@ class HistoryCache:
     lengths and the stack's height alternate between two buffers, since the
     library's calls read one and write the other; ``append`` and ``release``
     advance that state on the host, so inside a captured graph use the calls
-    themselves."""
+    themselves.  ``max_q`` is the most query rows that a captured ``attend`` may
+    have; an eager one with more raises it."""
 
     def __init__(self, dims: lime_kv_dims, B: int, max_q: int = 0, device="cuda"):
         self.dims, self.B = dims, B
@@ -257,7 +258,8 @@ class HistoryCache:
         self.free = torch.arange(dims.n_blocks - 1, -1, -1, dtype=torch.int32, device=device)
         self.lens, self._lens = new(B), new(B)
         self.n_free, self._n_free = new(1) + dims.n_blocks, new(1)
-        self.ws = KvWorkspace(dims, B, max_q, device=device)
+        # one workspace for the cache's life: a captured call keeps writing into it
+        self.ws = KvWorkspace(dims, B, max(1, max_q), device=device)
         self.max_q = max_q
 
     def _advance(self):
@@ -279,10 +281,8 @@ class HistoryCache:
         """Attention of Q [n, Hq, dh] over the cached rows; returns O [n, Hq, dh]."""
         if Q.shape[0] > self.max_q:
             if torch.cuda.is_current_stream_capturing():
-                raise ValueError("Q: more rows than max_q; a capture needs the workspace beforehand")
-            ws = KvWorkspace(self.dims, self.B, Q.shape[0], device=self.k.device)
-            ws.buf[:4].copy_(self.ws.buf[:4])       # flags that status() has not read yet
-            self.ws, self.max_q = ws, Q.shape[0]
+                raise ValueError("Q: more rows than max_q, the most that a captured call may have")
+            self.max_q = Q.shape[0]
         O = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
         lime_kv_attention(self.dims, Q, q_offsets, self.table, self.lens, self.k, self.v,
                           self.scale, O, lse, self.ws, sm_scale, causal)

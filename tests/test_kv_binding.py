@@ -1,0 +1,93 @@
+"""CPU-only checks of the history cache's binding: what it passes on, keeps and
+refuses.  The library's entry points are replaced by recorders, and host tensors
+stand for the current device's."""
+import pytest
+import torch
+
+from recsys_decoupled_link_b200 import build as lime_build
+
+
+class Recorder:
+    """Stands for the library: answers the size queries, records every other call."""
+
+    def __init__(self, lib):
+        self.lib, self.calls = lib, []
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return getattr(self.lib, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+    def names(self):
+        return [n for n, _ in self.calls]
+
+
+@pytest.fixture
+def kv(monkeypatch):
+    lime_build.build()
+    from recsys_decoupled_link_b200 import lime_kv as m
+    monkeypatch.setattr(m, "_lib", Recorder(m._lib))
+    monkeypatch.setattr(m, "_device", lambda: -1)                    # a host tensor's get_device()
+    monkeypatch.setattr(m, "_raw_stream", lambda stream, dev: 0)
+    return m
+
+
+@pytest.fixture
+def capturing(monkeypatch):
+    state = {"on": False}
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["on"])
+    return state
+
+
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def i64(*shape):
+    return torch.zeros(*shape, dtype=torch.int64)
+
+
+# ------------------------------------------------------------ history cache
+
+def make_cache(kv, B=2, **kw):
+    return kv.HistoryCache(kv.make_kv_dims(4, 2, 32, 16, 10, 4, "bf16"), B, device="cpu", **kw)
+
+
+def rows(n, heads):
+    return torch.zeros(n, heads, 32, dtype=torch.bfloat16)
+
+
+def test_workspace_of_one_query_row_serves_any_number(kv):
+    for B in (1, 2048, 2049, 100_000):
+        for dims in (kv.make_kv_dims(4, 2, 32, 16, 10, 4, "bf16"), kv.make_kv_dims(8, 8, 128, 64, 10, 4, "f32")):
+            one = kv.lime_kv_workspace_bytes(dims, B, 1)
+            assert one > 0
+            for n in (2, 1000, 2 ** 31 - 1):
+                assert kv.lime_kv_workspace_bytes(dims, B, n) == one
+
+
+@pytest.mark.parametrize("max_q", [0, 4])
+def test_cache_keeps_one_workspace(kv, capturing, max_q):
+    # what a captured call writes to must outlive every later call, whatever its size
+    cache = make_cache(kv, max_q=max_q)
+    ws, address = cache.ws, cache.ws.address
+    for n in (1, 4, 5, 300, 7):
+        cache.attend(rows(n, 4), i64(3))
+        assert cache.ws is ws and cache.ws.address == address == cache.ws.buf.data_ptr()
+    assert cache.max_q == 300
+    assert [n for n in kv._lib.names() if n != "lime_kv_attention"] == ["lime_kv_workspace_init"]
+    name, args = kv._lib.calls[-1]
+    assert args[-3] == address and args[-2] == ws.nbytes
+
+
+def test_cache_in_a_capture(kv, capturing):
+    cache = make_cache(kv, max_q=6)
+    capturing["on"] = True
+    cache.attend(rows(6, 4), i64(3))
+    with pytest.raises(ValueError, match="max_q"):
+        cache.attend(rows(7, 4), i64(3))
+    assert cache.max_q == 6
