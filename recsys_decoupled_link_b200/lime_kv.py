@@ -242,11 +242,11 @@ class HistoryCache:
     ``append`` finds room for new rows and writes them, ``attend`` lets query
     rows attend over everything cached, ``release`` shortens requests.  Calls
     are asynchronous on the current stream and belong on one stream.  The
-    lengths and the stack's height alternate between two buffers, since the
-    library's calls read one and write the other; ``append`` and ``release``
-    advance that state on the host, so inside a captured graph use the calls
-    themselves.  ``max_q`` is the most query rows that a captured ``attend`` may
-    have; an eager one with more raises it."""
+    library's calls read lengths and stack height from one buffer and write
+    another, which is then copied back: ``lens`` and ``n_free`` stay where they
+    are, so a captured call works on the cache as it stands at each replay.
+    ``max_q`` is the most query rows that a captured ``attend`` may have; an eager
+    one with more raises it."""
 
     def __init__(self, dims: lime_kv_dims, B: int, max_q: int = 0, device="cuda"):
         self.dims, self.B = dims, B
@@ -256,15 +256,16 @@ class HistoryCache:
         self.scale = torch.empty(dims.n_blocks, dims.Hkv, 2, device=device)
         self.table = new(B, dims.max_blocks) - 1
         self.free = torch.arange(dims.n_blocks - 1, -1, -1, dtype=torch.int32, device=device)
-        self.lens, self._lens = new(B), new(B)
-        self.n_free, self._n_free = new(1) + dims.n_blocks, new(1)
+        self._state, self._next = new(B + 1), new(B + 1)    # lengths, then the stack's height
+        self._state[B] = dims.n_blocks
+        self.lens, self.n_free = self._state[:B], self._state[B:]
+        self._lens, self._n_free = self._next[:B], self._next[B:]
         # one workspace for the cache's life: a captured call keeps writing into it
         self.ws = KvWorkspace(dims, B, max(1, max_q), device=device)
         self.max_q = max_q
 
     def _advance(self):
-        self.lens, self._lens = self._lens, self.lens
-        self.n_free, self._n_free = self._n_free, self.n_free
+        self._state.copy_(self._next)
 
     def append(self, K: torch.Tensor, V: torch.Tensor, new_offsets: torch.Tensor) -> torch.Tensor:
         """Caches K, V [n, Hkv, dh], request u's rows at [new_offsets[u], new_offsets[u+1]);

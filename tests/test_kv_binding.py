@@ -91,3 +91,20 @@ def test_cache_in_a_capture(kv, capturing):
     with pytest.raises(ValueError, match="max_q"):
         cache.attend(rows(7, 4), i64(3))
     assert cache.max_q == 6
+
+
+def test_cache_state_stays_where_it_is(kv):
+    cache = make_cache(kv)
+    lens, n_free = cache.lens, cache.n_free
+    at = lens.data_ptr(), n_free.data_ptr()
+    assert lens.tolist() == [0, 0] and n_free.tolist() == [10]
+    for step in range(1, 4):
+        cache._next.copy_(torch.tensor([step, 2 * step, 10 - step]))  # what the call would write
+        if step < 3:
+            cache.append(rows(5, 2), rows(5, 2), i64(3))
+        else:
+            cache.release()
+        assert cache.lens is lens and cache.n_free is n_free and at == (lens.data_ptr(), n_free.data_ptr())
+        assert lens.tolist() == [step, 2 * step] and n_free.tolist() == [10 - step]
+    fn, args = kv._lib.calls[-1]
+    assert fn == "lime_kv_release" and args[2] == at[0] and args[7] == at[1]
