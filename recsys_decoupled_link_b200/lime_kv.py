@@ -144,9 +144,9 @@ def lime_kv_reserve(dims, lens, new_offsets, block_table, free_blocks, n_free, l
     n, cap = slot_map.shape[0], free_blocks.shape[0]
     if not (lens.dtype is _i32 and new_offsets.dtype is _i64 and block_table.dtype is _i32
             and free_blocks.dtype is _i32 and n_free.dtype is _i32 and lens_out.dtype is _i32
-            and n_free_out.dtype is _i32 and slot_map.dtype is _i64
-            and new_offsets.numel() == B + 1 and block_table.numel() == B * dims.max_blocks
-            and n_free.numel() == 1 and lens_out.numel() == B and n_free_out.numel() == 1
+            and n_free_out.dtype is _i32 and slot_map.dtype is _i64 and lens.dim() == 1
+            and new_offsets.shape == (B + 1,) and block_table.shape == (B, dims.max_blocks)
+            and n_free.shape == (1,) and lens_out.shape == (B,) and n_free_out.shape == (1,)
             and lens.get_device() == dev and new_offsets.get_device() == dev
             and block_table.get_device() == dev and free_blocks.get_device() == dev
             and n_free.get_device() == dev and lens_out.get_device() == dev
@@ -212,8 +212,8 @@ def lime_kv_attention(dims, Q, q_offsets, block_table, lens, k_cache, v_cache, s
     shape = (n, dims.Hq, dims.dh)
     if not (Q.dtype is dt and O.dtype is dt and q_offsets.dtype is _i64
             and block_table.dtype is _i32 and lens.dtype is _i32 and Q.shape == shape
-            and O.shape == shape and q_offsets.numel() == B + 1
-            and block_table.numel() == B * dims.max_blocks
+            and O.shape == shape and lens.dim() == 1 and q_offsets.shape == (B + 1,)
+            and block_table.shape == (B, dims.max_blocks)
             and Q.get_device() == dev and O.get_device() == dev and q_offsets.get_device() == dev
             and block_table.get_device() == dev and lens.get_device() == dev
             and O.is_contiguous() and q_offsets.is_contiguous() and block_table.is_contiguous()

@@ -108,3 +108,66 @@ def test_cache_state_stays_where_it_is(kv):
         assert lens.tolist() == [step, 2 * step] and n_free.tolist() == [10 - step]
     fn, args = kv._lib.calls[-1]
     assert fn == "lime_kv_release" and args[2] == at[0] and args[7] == at[1]
+
+
+# --------------------------------------------------------- tensors of a call
+
+class Space:
+    """A workspace beside the host tensors that stand for device ones."""
+    device, address, nbytes = -1, 1 << 20, 1 << 30
+
+
+def call(kv, fn, **change):
+    """Calls `fn` with B = 3 requests; returns what reached the library, if anything did."""
+    d = kv.make_kv_dims(4, 2, 32, 16, 8, 5, "bf16")
+    pool = dict(k_cache=torch.zeros(8, 2, 16, 32, dtype=torch.int8), scale=torch.zeros(8, 2, 2))
+    pool["v_cache"] = pool["k_cache"].clone()
+    table = dict(block_table=i32(3, 5))
+    stack = dict(free_blocks=i32(8), n_free=i32(1), lens_out=i32(3), n_free_out=i32(1))
+    args = {"lime_kv_reserve": dict(lens=i32(3), new_offsets=i64(4), **table, **stack, slot_map=i64(6)),
+            "lime_kv_release": dict(lens=i32(3), keep=i32(3), **table, **stack),
+            "lime_kv_append": dict(K=rows(6, 2), V=rows(6, 2), slot_map=i64(6), **pool),
+            "lime_kv_attention": dict(Q=rows(6, 4), q_offsets=i64(4), **table, lens=i32(3), **pool, O=rows(6, 4),
+                                      lse=torch.zeros(6, 4))}[fn]
+    assert set(change) <= set(args)
+    args.update(change)
+    kv._lib.calls.clear()
+    getattr(kv, fn)(d, ws=Space, **args)
+    return kv._lib.calls
+
+
+CALLS = ["lime_kv_reserve", "lime_kv_release", "lime_kv_append", "lime_kv_attention"]
+
+
+@pytest.mark.parametrize("fn", CALLS)
+def test_calls_pass_on_what_they_document(kv, fn):
+    assert [n for n, _ in call(kv, fn)] == [fn]
+
+
+WRONG_SHAPES = {
+    "lens": [(3, 2), (6,), (1, 3), (3, 1)],
+    "new_offsets": [(3,), (1, 4), (4, 1), (2, 2)],
+    "q_offsets": [(3,), (1, 4), (4, 1), (2, 2)],
+    "block_table": [(5, 3), (15,), (3, 5, 1), (3, 4), (4, 5)],
+    "free_blocks": [(8, 1), (2, 4)],
+    "n_free": [(), (1, 1), (2,)],
+    "n_free_out": [(), (1, 1), (2,)],
+    "lens_out": [(3, 1), (1, 3), (4,)],
+    "keep": [(3, 1), (3, 2), (4,)],
+    "slot_map": [(6, 1), (1, 6)],
+    "lse": [(4, 6), (24,)],
+}
+
+
+@pytest.mark.parametrize("fn,name,shape", [(fn, name, shape) for fn, names in (
+    ("lime_kv_reserve", "lens new_offsets block_table free_blocks n_free n_free_out lens_out slot_map"),
+    ("lime_kv_release", "lens keep block_table free_blocks n_free n_free_out lens_out"),
+    ("lime_kv_append", "slot_map"),
+    ("lime_kv_attention", "lens q_offsets block_table lse")) for name in names.split() for shape in WRONG_SHAPES[name]])
+def test_calls_refuse_other_shapes(kv, fn, name, shape):
+    # among them shapes of as many elements, which would be read in another order
+    dtype = {"new_offsets": torch.int64, "q_offsets": torch.int64, "slot_map": torch.int64,
+             "lse": torch.float32}.get(name, torch.int32)
+    with pytest.raises(ValueError):
+        call(kv, fn, **{name: torch.zeros(shape, dtype=dtype)})
+    assert kv._lib.calls == []
