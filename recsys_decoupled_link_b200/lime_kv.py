@@ -133,7 +133,9 @@ def _check_pool(dims, dev, k_cache, v_cache, scale):
 
 
 def lime_kv_workspace_init(ws: KvWorkspace, stream=None):
-    rc = _lib.lime_kv_workspace_init(ws.address, ws.nbytes, _raw_stream(stream, _device()))
+    dev = _device()
+    _refuse(dev, ws)            # another device's work is not ordered behind this one's stream
+    rc = _lib.lime_kv_workspace_init(ws.address, ws.nbytes, _raw_stream(stream, dev))
     if rc:
         raise LimeError("lime_kv_workspace_init", rc)
 
@@ -296,4 +298,5 @@ class HistoryCache:
         self._advance()
 
     def status(self, stream=None) -> int:
+        _refuse(_device(), self.ws)
         return lime_get_status(self.ws, stream)

@@ -171,3 +171,15 @@ def test_calls_refuse_other_shapes(kv, fn, name, shape):
     with pytest.raises(ValueError):
         call(kv, fn, **{name: torch.zeros(shape, dtype=dtype)})
     assert kv._lib.calls == []
+
+
+def test_a_workspace_is_initialised_on_its_own_device(kv, monkeypatch):
+    # from another device's stream it would be cleared beside the calls that use it
+    dims, cache = kv.make_kv_dims(4, 2, 32, 16, 10, 4, "bf16"), make_cache(kv)
+    monkeypatch.setattr(kv, "lime_get_status", lambda ws, stream: 3)
+    assert kv._lib.names() == ["lime_kv_workspace_init"] and cache.status() == 3
+    monkeypatch.setattr(kv, "_device", lambda: 1)
+    for make in (lambda: kv.KvWorkspace(dims, 2, 1, device="cpu"), lambda: make_cache(kv), cache.status):
+        with pytest.raises(ValueError, match="current device"):
+            make()
+    assert kv._lib.names() == ["lime_kv_workspace_init"]
