@@ -118,7 +118,7 @@ def _pitch(name: str, t: torch.Tensor, heads: int, dh: int) -> int:
     ld, sh, sd = t.stride()
     if sd != 1 or (sh != dh and heads > 1):
         raise ValueError(f"{name}: the heads of a row have to be contiguous")
-    return ld if t.shape[0] > 1 else max(ld, heads * dh)
+    return ld if t.shape[0] > 1 else heads * dh     # one row has no pitch
 
 
 def _check_pool(dims, dev, k_cache, v_cache, scale):

@@ -41,3 +41,16 @@ def test_captured_attention_outlives_a_larger_eager_one(dh, n_rows):
     assert torch.equal(out, want)
     assert all(bool((f == 7).all()) for f in fillers)
     assert cache.status() == 0 and torch.equal(cache.attend(q, off), want)
+
+
+def test_a_single_row_of_any_pitch():
+    # the only row of a wider buffer whose width is no multiple of 16 bytes
+    dims = lime_kv.make_kv_dims(2, 2, 32, 16, 4, 2, "bf16")
+    outs = []
+    for pitch in (64, 65, 3):
+        cache = lime_kv.HistoryCache(dims, 1, max_q=1)
+        at = lambda seed: rows(64, seed=seed).as_strided((1, 2, 32), (pitch, 32, 1))
+        cache.append(at(1), at(2), offsets([1]))
+        outs.append(cache.attend(at(3), offsets([1])))
+        assert cache.status() == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and bool((outs[0] != 0).any())

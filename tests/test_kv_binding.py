@@ -183,3 +183,14 @@ def test_a_workspace_is_initialised_on_its_own_device(kv, monkeypatch):
         with pytest.raises(ValueError, match="current device"):
             make()
     assert kv._lib.names() == ["lime_kv_workspace_init"]
+
+
+@pytest.mark.parametrize("pitch", [0, 3, 64, 65, 2 ** 33])
+def test_the_pitch_of_a_single_row_does_not_matter(kv, pitch):
+    one = torch.zeros(64, dtype=torch.bfloat16).as_strided((1, 2, 32), (pitch, 32, 1))
+    assert kv._pitch("K", one, 2, 32) == 64
+    (_, args), = call(kv, "lime_kv_append", K=one, V=one, slot_map=i64(1))
+    assert args[2] == args[4] == 64
+    q = torch.zeros(128, dtype=torch.bfloat16).as_strided((1, 4, 32), (pitch, 32, 1))
+    (_, args), = call(kv, "lime_kv_attention", Q=q, O=rows(1, 4), lse=torch.zeros(1, 4))
+    assert args[3] == 128
