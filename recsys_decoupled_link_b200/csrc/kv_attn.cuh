@@ -340,9 +340,10 @@ __device__ __forceinline__ void row_scale(const Args& a, float top, float* s1, f
 }
 
 // log2 of a value scale over the unit, at least -60 (what is smaller adds
-// nothing), and the factor that takes it out of a sum again.
+// nothing), and the factor that takes it out of a sum again.  Both may be any
+// finite numbers: the fast division gives 0 for a unit above 2^126.
 __device__ __forceinline__ void unit_log2(float vs, float unit, float* lr, float* inv) {
-  const float ratio = __log2f(__fdividef(vs, unit));
+  const float ratio = __log2f(__fdiv_rn(vs, unit));
   *lr = unit > 0.0f ? (ratio > -60.0f ? ratio : -60.0f) : 0.0f;
   *inv = ex2(-*lr);
 }
