@@ -299,20 +299,24 @@ __device__ __forceinline__ void join_parts(const Args& a, int first, int last, i
       float best = top;
 #pragma unroll
       for (int c = 0; c < kJoin; ++c) best = fmaxf(best, x[c].x);
-      const float ref = best == -INFINITY ? 0.0f : best, keep = ex2(top - ref);
-      sum *= keep;
-      v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+      // v stays normalised: outputs near fp32's largest would overflow times a sum
+      const float ref = best == -INFINITY ? 0.0f : best;
+      float keep = sum * ex2(top - ref);
+      sum = keep;
+#pragma unroll
+      for (int c = 0; c < kJoin; ++c) sum += x[c].y *= ex2(x[c].x - ref);
       top = best;
+      const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+      keep *= by;
+      v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
 #pragma unroll
       for (int c = 0; c < kJoin; ++c) {
-        const float k = x[c].y * ex2(x[c].x - ref);
-        sum += k;
+        const float k = x[c].y * by;
         v.x = fmaf(k, y[c].x, v.x), v.y = fmaf(k, y[c].y, v.y);
         v.z = fmaf(k, y[c].z, v.z), v.w = fmaf(k, y[c].w, v.w);
       }
     }
-    const float by = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-    store(r, d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by), top, sum);
+    store(r, d, v, top, sum);
   }
 }
 

@@ -37,6 +37,16 @@ def test_attention_value_scales_near_the_largest_float(dtype, low):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("low", [9e37, 1e30, 1.0])
+def test_attention_joins_values_near_the_largest_float(dtype, low):
+    # rows cut at workers' borders: short ones, and one over many workers (more than are joined at a time)
+    check_attention([5, 40], [100, 13], 4, 2, 32, 16, dtype, hook=near_the_largest(low))
+    check_attention([1, 1], [100, 13], 4, 2, 128, 16, dtype, hook=near_the_largest(low), seed=1)
+    check_attention([3], [7001], 4, 2, 64, 64, dtype, hook=near_the_largest(low), seed=2)
+    check_attention([2, 33], [9000, 70], 2, 1, 32, 64, dtype, hook=near_the_largest(low), seed=3, causal=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dh", [32, 128])
 @pytest.mark.parametrize("unit,low", [(1e-39, 1e-39), (1e-39, 1e-41), (3e-38, 1e-39), (1e-41, 1e-42)])
 def test_attention_value_scales_below_the_normal_range(dtype, dh, unit, low):
