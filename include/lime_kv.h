@@ -96,7 +96,8 @@ int lime_kv_reserve(const lime_kv_dims* dims, int64_t B, const int32_t* lens,
  * Blocks that hold no kept row go onto the stack in the order of the requests
  * and of their rows, and their table entries become -1.  Arguments as in
  * lime_kv_reserve; free_blocks is written from n_free on, up to free_cap
- * (what would pass it is dropped and LIME_FLAG_BAD_BLOCK set). */
+ * (what would pass it is dropped and LIME_FLAG_BAD_BLOCK set).  An entry
+ * outside the pool does not go onto the stack and sets LIME_FLAG_BAD_BLOCK. */
 int lime_kv_release(const lime_kv_dims* dims, int64_t B, const int32_t* lens,
                     const int32_t* keep, int32_t* block_table, int32_t* free_blocks,
                     int64_t free_cap, const int32_t* n_free, int32_t* lens_out,

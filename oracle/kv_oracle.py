@@ -35,13 +35,15 @@ def reserve(lens, new, table, free, n_free, bs):
     return np.array(out), n_free - used, table, np.array(slots, dtype=np.int64), refused
 
 
-def release(lens, keep, table, free, n_free, bs):
-    """Returns (lens_out, free_out (the stack's live part), table_out)."""
+def release(lens, keep, table, free, n_free, bs, n_blocks=None):
+    """Returns (lens_out, free_out (the stack's live part), table_out).  With n_blocks, table
+    entries outside the pool are dropped."""
     table, stack, out = np.array(table), list(free[:n_free]), []
     for u, n in enumerate(map(int, lens)):
         k = 0 if keep is None else min(max(int(keep[u]), 0), n)
         for c in range(blocks_of(k, bs), blocks_of(n, bs)):
-            stack.append(int(table[u, c]))
+            if n_blocks is None or 0 <= table[u, c] < n_blocks:
+                stack.append(int(table[u, c]))
             table[u, c] = -1
         out.append(k)
     return np.array(out), np.array(stack, dtype=np.int64), table

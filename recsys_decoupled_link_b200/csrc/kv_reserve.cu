@@ -286,27 +286,56 @@ __device__ __forceinline__ int kept_rows(const int32_t* keep, int64_t u, int n) 
   return k < 0 ? 0 : (k < n ? k : n);
 }
 
+// Table columns [c0, c1) whose blocks request u gives back.
+__device__ __forceinline__ void released(const int32_t* lens, const int32_t* keep, int64_t u, int bs, int max_blocks,
+                                         unsigned* status, int* rows, int64_t* c0, int64_t* c1) {
+  const int n = kv_len(lens, u, (int64_t)max_blocks * bs, status);
+  *rows = kept_rows(keep, u, n);
+  *c0 = ceil_div(*rows, bs);
+  *c1 = ceil_div(n, bs);
+}
+
+// A warp per request counts the blocks it gives back.  Entries outside the pool
+// are no blocks: on the stack they would be handed out again and again.
+__global__ void k_release_count(int64_t B, int bs, int max_blocks, int64_t n_blocks, const int32_t* lens,
+                                const int32_t* keep, const int32_t* table, int32_t* lens_out, int64_t* first,
+                                unsigned* status) {
+  const int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (u >= B) return;
+  int rows;
+  int64_t c0, c1;
+  released(lens, keep, u, bs, max_blocks, status, &rows, &c0, &c1);
+  int count = 0;
+  bool odd = false;
+  for (int64_t c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
+    const int32_t id = table[u * max_blocks + c];
+    const bool ok = id >= 0 && id < n_blocks;
+    count += ok;
+    odd |= !ok;
+  }
+  if (odd) raise_flag(status, LIME_FLAG_BAD_BLOCK);
+  count = __reduce_add_sync(0xffffffffu, count);
+  if ((threadIdx.x & 31) == 0) {
+    first[u] = count;
+    lens_out[u] = rows;
+  }
+}
+
+// first[u]: from the number of blocks that u gives back to the place of the first.
 __global__ void __launch_bounds__(kScanThreads)
-    k_release_scan(int64_t B, int bs, int max_blocks, const int32_t* lens, const int32_t* keep,
-                   int64_t cap, const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out,
-                   int64_t* first, unsigned* status) {
-  const int64_t most = (int64_t)max_blocks * bs;
+    k_release_scan(int64_t B, int64_t cap, const int32_t* n_free, int32_t* n_free_out, int64_t* first,
+                   unsigned* status) {
   const int64_t per = ceil_div(B, kScanThreads);
   const int64_t u0 = per * threadIdx.x, u1 = u0 + per < B ? u0 + per : B;
   const int height = stack_height(n_free, cap, status);
   int64_t sum = 0;
-  for (int64_t u = u0; u < u1; ++u) {
-    const int n = kv_len(lens, u, most, status);
-    sum += ceil_div(n, bs) - ceil_div(kept_rows(keep, u, n), bs);
-  }
+  for (int64_t u = u0; u < u1; ++u) sum += first[u];
   int64_t all;
   int64_t at = height + block_scan<kScanThreads>(sum, &all);
   for (int64_t u = u0; u < u1; ++u) {
-    const int n = kv_len(lens, u, most, status);
-    const int k = kept_rows(keep, u, n);
+    const int64_t count = first[u];
     first[u] = at;
-    at += ceil_div(n, bs) - ceil_div(k, bs);
-    lens_out[u] = k;
+    at += count;
   }
   if (threadIdx.x == 0) {
     if (height + all > cap) raise_flag(status, LIME_FLAG_BAD_BLOCK);
@@ -315,17 +344,24 @@ __global__ void __launch_bounds__(kScanThreads)
 }
 
 // A warp per request pushes its released blocks.
-__global__ void k_release_fill(int64_t B, int bs, int max_blocks, const int32_t* lens,
-                               const int32_t* keep, int32_t* table, int32_t* free_blocks,
-                               int64_t cap, const int64_t* first, unsigned* status) {
+__global__ void k_release_fill(int64_t B, int bs, int max_blocks, int64_t n_blocks, const int32_t* lens,
+                               const int32_t* keep, int32_t* table, int32_t* free_blocks, int64_t cap,
+                               const int64_t* first, unsigned* status) {
   const int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (u >= B) return;
-  const int n = kv_len(lens, u, (int64_t)max_blocks * bs, status);
-  const int64_t c0 = ceil_div(kept_rows(keep, u, n), bs), c1 = ceil_div(n, bs);
-  for (int64_t c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
-    const int64_t at = first[u] + (c - c0);
-    if (at < cap) free_blocks[at] = table[u * max_blocks + c];
-    table[u * max_blocks + c] = -1;
+  const int lane = threadIdx.x & 31;
+  int rows;
+  int64_t c0, c1, at = first[u];
+  released(lens, keep, u, bs, max_blocks, status, &rows, &c0, &c1);
+  for (; c0 < c1; c0 += 32) {
+    const int64_t c = c0 + lane;
+    const int32_t id = c < c1 ? table[u * max_blocks + c] : -1;
+    const bool ok = id >= 0 && id < n_blocks;
+    const unsigned good = __ballot_sync(0xffffffffu, ok);
+    const int64_t to = at + __popc(good & ((1u << lane) - 1u));
+    if (ok && to < cap) free_blocks[to] = id;
+    if (c < c1) table[u * max_blocks + c] = -1;
+    at += __popc(good);
   }
 }
 
@@ -364,13 +400,17 @@ int kv_release(const lime_kv_dims& D, int64_t B, const int32_t* lens, const int3
                int32_t* lens_out, int32_t* n_free_out, void* ws, unsigned* status,
                cudaStream_t st) {
   int64_t* first = (int64_t*)ws;
-  k_release_scan<<<1, kScanThreads, 0, st>>>(B, D.block, D.max_blocks, lens, keep, free_cap,
-                                             n_free, lens_out, n_free_out, first, status);
+  const unsigned grid = (unsigned)ceil_div(B, 8);
+  if (B > 0) {
+    k_release_count<<<grid, 256, 0, st>>>(B, D.block, D.max_blocks, D.n_blocks, lens, keep, table, lens_out, first,
+                                          status);
+    note_launches(1);
+  }
+  k_release_scan<<<1, kScanThreads, 0, st>>>(B, free_cap, n_free, n_free_out, first, status);
   note_launches(1);
   if (B > 0) {
-    k_release_fill<<<(unsigned)ceil_div(B, 8), 256, 0, st>>>(B, D.block, D.max_blocks, lens, keep,
-                                                             table, free_blocks, free_cap, first,
-                                                             status);
+    k_release_fill<<<grid, 256, 0, st>>>(B, D.block, D.max_blocks, D.n_blocks, lens, keep, table, free_blocks,
+                                         free_cap, first, status);
     note_launches(1);
   }
   return LIME_OK;
