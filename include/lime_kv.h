@@ -83,7 +83,9 @@ int lime_kv_workspace_init(void* workspace, size_t bytes, cudaStream_t stream);
  * their rows.  A request that does not get all it needs (the stack is too
  * short for it and the requests before it, or its rows pass max_blocks) gets
  * none: its slots are -1, its length stays, LIME_FLAG_NO_BLOCKS is set;
- * requests that need no new block are served all the same.
+ * requests that need no new block are served all the same.  What a request
+ * refused for want of blocks asked for counts for those behind it: none of them
+ * that needs a block is served, even where enough for it are left.
  * Outputs may not overlap inputs or each other (LIME_ERR_ALIAS). */
 int lime_kv_reserve(const lime_kv_dims* dims, int64_t B, const int32_t* lens,
                     const int64_t* new_offsets, int64_t total_new, int32_t* block_table,
@@ -139,12 +141,18 @@ int lime_kv_append(const lime_kv_dims* dims, const void* K, int64_t ldk, const v
  *                the rows j <= lens[u] - m + i
  *   O            device [total_q, Hq, dh], contiguous
  *   lse          device fp32 [total_q, Hq] or NULL: log of the softmax's sum
- * |sm_scale| <= 2^100; scales are finite and not negative.  A query that sees
+ * |sm_scale| <= 2^100; scales are finite and not negative, and |sm_scale| times
+ * a row's largest |q| times a key scale stays below 2^127.  A query that sees
  * no row gets a zero output and lse = -inf.  Scores, sums and outputs are fp32.
- * Queries enter the score product exactly (bf16) or as two fp16 terms (fp32);
- * probabilities enter the value product as one fp16 term (bf16 dtype) or two
+ * A query row enters the score product as fp16 terms, under a power of two that
+ * brings its largest magnitude m to [2^14, 2^15): one term (bf16), which holds
+ * elements from 2^-31 m on exactly, or two (fp32), off by up to 2^-22 of the
+ * element.  Beside that an element is off by up to 2^-39 m, so a score by up to
+ * |sm_scale| 2^-39 m sum_d |k_d|, even where the keys are 0 in m's own dim.
+ * Probabilities enter the value product as one fp16 term (bf16 dtype) or two
  * (fp32), each times its block's value scale over the largest such scale among
- * the request's blocks, to 2^-39 of the row's largest probability: what weighs
+ * the request's blocks (seen by the row or not), to 2^-39 of the row's largest
+ * probability; one fp16 term loses bits from 2^-28 down.  What weighs
  * less is lost, so an output is off by up to 2^-39 of the request's largest
  * value for each row.  Codes behind a request's last row
  * are never used.  A table entry outside the pool hides its rows and sets

@@ -11,7 +11,7 @@ import torch
 
 from oracle import kv_oracle as K
 from recsys_decoupled_link_b200 import lime, lime_kv
-from test_gpu_kv import DT, U, check_attention, f64, i32, make_pool, offsets
+from test_gpu_kv import DT, U, assert_near, check_attention, f64, i32, make_pool, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,34 @@ def test_attention_value_scales_below_the_normal_range(dtype, dh, unit, low):
     err = np.abs(f64(O) - ref)
     assert (err <= tol).all(), (err / tol).max()
     assert np.abs(ref).max() > 0.3 * unit
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("top,exact", [(2.0 ** 20, True), (2.0 ** 30, False), (2.0 ** 33, False)])
+def test_attention_one_huge_query_dim_over_zero_keys(dtype, causal, top, exact):
+    """A row's largest element m sets the step of all others: 2^-39 m at most, which moves a score by
+    sm_scale 2^-39 m sum_d |k_d| although the keys are 0 there.  bf16 elements from 2^-31 m on are exact."""
+    rng = np.random.default_rng(11)
+    counts, lens, bs, dh, Hq, Hkv = [20, 1, 7], [300, 40, 5], 16, 32, 4, 2
+    table, codes, scale = make_pool(rng, lens, Hkv, dh, bs)
+    codes[0, ..., 3] = 0
+    q = rng.standard_normal((28, Hq, dh))
+    q = np.sign(q) * (0.25 + np.abs(q))
+    q[..., 3] = top * rng.choice([-1.0, 1.0], (28, Hq))
+    q = torch.tensor(q).to(DT[dtype])
+    dims = lime_kv.make_kv_dims(Hq, Hkv, dh, bs, codes.shape[1], table.shape[1], dtype)
+    ws = lime_kv.KvWorkspace(dims, 3, 28)
+    O, lse = torch.empty(28, Hq, dh, dtype=q.dtype, device="cuda"), torch.empty(28, Hq, device="cuda")
+    lime_kv.lime_kv_attention(dims, q.cuda(), offsets(counts), i32(table), i32(lens),
+                              torch.tensor(codes[0], device="cuda"), torch.tensor(codes[1], device="cuda"),
+                              torch.tensor(scale, device="cuda"), O, lse, ws, causal=causal)
+    assert lime.lime_get_status(ws) == 0
+    finite = np.nan_to_num(scale).astype(np.float64)
+    ref, rl, A, S, V = K.attention(f64(q), counts, table, lens, codes[0], codes[1], finite, bs, dh ** -0.5, causal)
+    # |k_d| summed over the dims: S of a query of ones
+    ones = K.attention(np.ones((28, Hq, dh)), counts, table, lens, codes[0], codes[1], finite, bs, dh ** -0.5,
+                       causal)[3]
+    step = np.zeros_like(S) if exact and dtype == "bf16" else 2.0 ** -39 * top * ones
+    # test_gpu_kv.py's bound takes a score to be off by S (dh + 8) 2u
+    assert_near(O, lse, ref, rl, A, S + step / ((dh + 8) * 2 * U), V, max(lens), dh, dtype)
