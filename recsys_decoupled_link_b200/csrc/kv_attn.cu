@@ -214,6 +214,13 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
               const Args a) {
   constexpr bool kSplit = sizeof(T) == 4;  // fp32 rows: operands as two fp16 terms
   constexpr int NQ = kSplit ? 2 : 1;
+  // A tensor core's adds truncate, which over thousands of keys costs fp32 outputs
+  // more than all else: single queries over 4,096 keys of 32 dims are 1.4e-6 of their
+  // size off, and 4e-7 with a step's products summed apart, added with rounding, and
+  // the scores' small terms summed first.  That takes 5 to 8 % more time (32 links over
+  // 2,048 rows 72.5 to 78 us).  Heads of 128 have no registers for sums apart; the
+  // scores' order alone brings them to 7.5e-7 (from 1.3e-6), for 3 to 6 %.
+  constexpr bool kApart = kSplit && DH <= 64;
   constexpr int TK = Tile<DH>::TK, SK = Tile<DH>::SK, S = Tile<DH>::kStages, NG = SK / 16;
   constexpr int kGroups = kWarps / NW;     // workers of a block
   constexpr int NC = ONE ? 1 : NG;         // scales of a step
@@ -476,17 +483,36 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
 #pragma unroll
           for (int c = 0; c < E; c += 16)
             lds<E < 16 ? E : 16>(ks + sub * DH + (swz_at(k_at, row) ^ c ^ flip), w + c / 4);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
+          auto key_frags = [&](int k, uint32_t& b0, uint32_t& b1) {
             const uint32_t b = w[k] ^ 0x80808080u;
-            const uint32_t b0 = codes_to_half2<0x4140>(b), b1 = codes_to_half2<0x4342>(b);
+            b0 = codes_to_half2<0x4140>(b), b1 = codes_to_half2<0x4342>(b);
+          };
+          if constexpr (kSplit) {
+            // second terms first: a tensor core's adds truncate, and onto a whole
+            // score that of a small term costs as much as a large one's
+            uint32_t b0[KS], b1[KS];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int k = 0; k < KS; ++k) key_frags(k, b0[k], b1[k]);
 #pragma unroll
-              for (int p = 0; p < NQ; ++p) {
-                if (k + p == 0) mma16816_first(s[mt][x], qf[mt][k][p], b0, b1);
-                else mma16816(s[mt][x], qf[mt][k][p], b0, b1);
+            for (int p = NQ - 1; p >= 0; --p)
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  if (p == NQ - 1 && k == 0) mma16816_first(s[mt][x], qf[mt][k][p], b0[k], b1[k]);
+                  else mma16816(s[mt][x], qf[mt][k][p], b0[k], b1[k]);
+                }
+          } else {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              uint32_t b0, b1;
+              key_frags(k, b0, b1);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                if (k == 0) mma16816_first(s[mt][x], qf[mt][k][0], b0, b1);
+                else mma16816(s[mt][x], qf[mt][k][0], b0, b1);
               }
+            }
           }
         }
 
@@ -587,10 +613,8 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
         }
 
         // ---- values
-#pragma unroll
-        for (int x = 0; x < NG; ++x) {
-          constexpr int W = VB < 4 ? 1 : VB / 4;
-          uint32_t w[4][W];
+        constexpr int W = VB < 4 ? 1 : VB / 4, NI = VB < 4 ? VB : 4;
+        auto load_values = [&](int x, uint32_t (&w)[4][W]) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             lds<VB>(vs + sub * DH +
@@ -599,20 +623,64 @@ __global__ void __launch_bounds__(kWarps * 32, min_blocks<T, DH, MT>())
 #pragma unroll
             for (int c = 0; c < W; ++c) w[i][c] ^= 0x80808080u;
           }
+        };
+        // fragments of dims 4 c + i: bytes of two keys side by side, two dims at a time
+        auto value_frags = [&](uint32_t (&w)[4][W], int c, int i, uint32_t& b0, uint32_t& b1) {
+          const uint32_t ab = __byte_perm(w[0][c], w[1][c], i < 2 ? 0x5140 : 0x7362);
+          const uint32_t cd = __byte_perm(w[2][c], w[3][c], i < 2 ? 0x5140 : 0x7362);
+          b0 = (i & 1) ? codes_to_half2<0x4342>(ab) : codes_to_half2<0x4140>(ab);
+          b1 = (i & 1) ? codes_to_half2<0x4342>(cd) : codes_to_half2<0x4140>(cd);
+        };
+        if constexpr (kApart) {
+          uint32_t w[NG][4][W];
+#pragma unroll
+          for (int x = 0; x < NG; ++x) load_values(x, w[x]);
 #pragma unroll
           for (int c = 0; c < W; ++c) {
-            // bytes of two keys side by side, two dims at a time
-            const uint32_t ab0 = __byte_perm(w[0][c], w[1][c], 0x5140), cd0 = __byte_perm(w[2][c], w[3][c], 0x5140);
-            const uint32_t ab1 = __byte_perm(w[0][c], w[1][c], 0x7362), cd1 = __byte_perm(w[2][c], w[3][c], 0x7362);
 #pragma unroll
-            for (int i = 0; i < (VB < 4 ? VB : 4); ++i) {
-              const uint32_t ab = i < 2 ? ab0 : ab1, cd = i < 2 ? cd0 : cd1;
-              const uint32_t b0 = (i & 1) ? codes_to_half2<0x4342>(ab) : codes_to_half2<0x4140>(ab);
-              const uint32_t b1 = (i & 1) ? codes_to_half2<0x4342>(cd) : codes_to_half2<0x4140>(cd);
+            for (int i = 0; i < NI; ++i) {
+              float part[MT][4];
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
+              for (int x = 0; x < NG; ++x) {
+                uint32_t b0, b1;
+                value_frags(w[x], c, i, b0, b1);
 #pragma unroll
-                for (int p = 0; p < NQ; ++p) mma16816(o[mt][4 * c + i], pf[mt][x][p], b0, b1);
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                  for (int p = 0; p < NQ; ++p) {
+                    if (x + p == 0) mma16816_first(part[mt], pf[mt][x][p], b0, b1);
+                    else mma16816(part[mt], pf[mt][x][p], b0, b1);
+                  }
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                float* to = o[mt][4 * c + i];
+#pragma unroll
+                for (int k = 0; k < 4; k += 2)
+                  unpack2(add2(pack2(to[k], to[k + 1]), pack2(part[mt][k], part[mt][k + 1])), to[k], to[k + 1]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < NG; ++x) {
+            uint32_t w[4][W];
+            load_values(x, w);
+#pragma unroll
+            for (int c = 0; c < W; ++c) {
+              // bytes of two keys side by side, two dims at a time
+              const uint32_t ab0 = __byte_perm(w[0][c], w[1][c], 0x5140), cd0 = __byte_perm(w[2][c], w[3][c], 0x5140);
+              const uint32_t ab1 = __byte_perm(w[0][c], w[1][c], 0x7362), cd1 = __byte_perm(w[2][c], w[3][c], 0x7362);
+#pragma unroll
+              for (int i = 0; i < NI; ++i) {
+                const uint32_t ab = i < 2 ? ab0 : ab1, cd = i < 2 ? cd0 : cd1;
+                const uint32_t b0 = (i & 1) ? codes_to_half2<0x4342>(ab) : codes_to_half2<0x4140>(ab);
+                const uint32_t b1 = (i & 1) ? codes_to_half2<0x4342>(cd) : codes_to_half2<0x4140>(cd);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                  for (int p = 0; p < NQ; ++p) mma16816(o[mt][4 * c + i], pf[mt][x][p], b0, b1);
+              }
             }
           }
         }
