@@ -116,7 +116,7 @@ def _row_dtype(dims):
 def _pitch(name: str, t: torch.Tensor, heads: int, dh: int) -> int:
     """Elements between the rows of t [n, heads, dh], whose heads have to be contiguous."""
     ld, sh, sd = t.stride()
-    if sd != 1 or (sh != dh and heads > 1):
+    if (sd != 1 or (sh != dh and heads > 1)) and t.shape[0] > 0:
         raise ValueError(f"{name}: the heads of a row have to be contiguous")
     return ld if t.shape[0] > 1 else heads * dh     # one row has no pitch
 

@@ -54,3 +54,15 @@ def test_a_single_row_of_any_pitch():
         outs.append(cache.attend(at(3), offsets([1])))
         assert cache.status() == 0
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and bool((outs[0] != 0).any())
+
+
+def test_a_step_without_new_rows():
+    dims = lime_kv.make_kv_dims(4, 2, 32, 16, 10, 4, "bf16")
+    cache = lime_kv.HistoryCache(dims, 2, max_q=4)
+    x = rows(5, 2, 2, 32, seed=1)
+    cache.append(x[:, 0], x[:, 1], offsets([5, 0]))
+    none = torch.zeros(0, 2, 2, 32, dtype=torch.bfloat16)
+    assert cache.append(none[:, 0].cuda(), none[:, 1].cuda(), offsets([0, 0])).numel() == 0
+    assert cache.lens.tolist() == [5, 0] and int(cache.n_free) == 9 and cache.status() == 0
+    out = cache.attend(rows(0, 4, 32, seed=2), offsets([0, 0]))
+    assert out.shape == (0, 4, 32) and cache.status() == 0

@@ -194,3 +194,16 @@ def test_the_pitch_of_a_single_row_does_not_matter(kv, pitch):
     q = torch.zeros(128, dtype=torch.bfloat16).as_strided((1, 4, 32), (pitch, 32, 1))
     (_, args), = call(kv, "lime_kv_attention", Q=q, O=rows(1, 4), lse=torch.zeros(1, 4))
     assert args[3] == 128
+
+
+def test_the_strides_of_no_rows_do_not_matter(kv):
+    # a slice of nothing, brought to another device, has strides of its own
+    none = torch.zeros(0, 2, 4, 32, dtype=torch.bfloat16)[:, 1].transpose(0, 1).contiguous().transpose(0, 1)
+    odd = torch.zeros(64, dtype=torch.bfloat16).as_strided((0, 4, 32), (1, 1, 7))
+    for q in (none, odd):
+        (_, args), = call(kv, "lime_kv_attention", Q=q, O=rows(0, 4), lse=torch.zeros(0, 4))
+        assert args[3] == 128 and args[5] == 0
+        (_, args), = call(kv, "lime_kv_append", K=q[:, :2], V=q[:, :2], slot_map=i64(0))
+        assert args[2] == args[4] == 64 and args[5] == 0
+    with pytest.raises(ValueError, match="contiguous"):
+        call(kv, "lime_kv_append", K=rows(6, 4)[:, ::2], V=rows(6, 2))
