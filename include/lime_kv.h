@@ -153,8 +153,8 @@ int lime_kv_append(const lime_kv_dims* dims, const void* K, int64_t ldk, const v
  * (fp32), each times its block's value scale over the largest such scale among
  * the request's blocks (seen by the row or not), to 2^-39 of the row's largest
  * probability; one fp16 term loses bits from 2^-28 down.  What weighs less is
- * lost, so an output is off by up to 2^-39 times 127 of the request's largest
- * value scales for each row.  Codes behind a request's last row
+ * lost, so for each row an output is off by up to 2^-39 * 127 times the largest
+ * value scale among the request's blocks.  Codes behind a request's last row
  * are never used.  A table entry outside the pool hides its rows and sets
  * LIME_FLAG_BAD_BLOCK. */
 int lime_kv_attention(const lime_kv_dims* dims, int64_t B, const void* Q, int64_t ldq,
